@@ -567,6 +567,8 @@ mf_status mf_sync_status(mf_stream_t stream) {
   if (v & kStatusCapacity) return fail(MF_ERR_CAPACITY, "kept blocks exceed nnz_capacity");
   if (v & kStatusBadCache)
     return fail(MF_ERR_INVALID_ARG, "a cache row holds more entries than its query block has key blocks");
+  if (v & kStatusBadPage)
+    return fail(MF_ERR_INVALID_ARG, "a token's place lies outside the page table or the page pool");
   return MF_OK;
 }
 

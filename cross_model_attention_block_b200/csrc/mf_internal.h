@@ -11,7 +11,7 @@
 namespace mf {
 
 // Bits of the per-device status word.
-enum : unsigned { kStatusTimeout = 1u, kStatusCapacity = 2u, kStatusBadCache = 4u };
+enum : unsigned { kStatusTimeout = 1u, kStatusCapacity = 2u, kStatusBadCache = 4u, kStatusBadPage = 8u };
 
 // Device address of the status word of the current device.
 unsigned* status_word();
@@ -132,5 +132,8 @@ cudaError_t launch_mapped_av_simt(const mf_csr_cache& c, const mf_attn_desc& d,
                                   const Sizes& sz, int Hr, const void* W,
                                   const mf_v_desc& v, void* O, int64_t qb_lo, int64_t qb_hi,
                                   cudaStream_t st);
+
+// Checks of a paged key-value cache that do not depend on the call.
+mf_status check_kv_cache(const mf_kv_cache* c);
 
 }  // namespace mf

@@ -31,6 +31,8 @@ EXPORTED = [
     "mf_select_rounds_workspace", "mf_select_rounds", "mf_cache_offload", "mf_cache_fetch",
     "mf_mapped_av_workspace", "mf_mapped_av", "mf_mapped_av_range", "mf_block_stats_noalloc",
     "mf_block_stats_noalloc_max_workspace",
+    "mf_rope_freqs", "mf_rope_phases", "mf_rope", "mf_kv_append", "mf_paged_attn_workspace",
+    "mf_paged_attn",
     "mf_mapped_av_plan", "mf_path_info", "mf_exp2_fma_eval", "mf_selftest_timeout", "mf_sync_status", "mf_prefix_hash",
     "mf_index_create",
     "mf_index_destroy",
@@ -57,6 +59,28 @@ class VDesc(C.Structure):
     _fields_ = [("V", C.c_void_p), ("page_table", C.c_void_p), ("page_size", C.c_int32),
                 ("max_pages_per_seq", C.c_int32), ("npages", C.c_int64), ("Hkv", C.c_int32),
                 ("d", C.c_int32)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("phases", C.c_void_p),
+                ("scale", C.c_float)]
+
+
+class TokenBatch(C.Structure):
+    _fields_ = [("ntok", C.c_int64), ("nseq", C.c_int32), ("cu_seqlens", C.c_void_p),
+                ("start", C.c_void_p)]
+
+
+class KvCacheDesc(C.Structure):
+    _fields_ = [("K", C.c_void_p), ("V", C.c_void_p), ("page_table", C.c_void_p),
+                ("npages", C.c_int64), ("page_size", C.c_int32),
+                ("max_pages_per_seq", C.c_int32), ("nseq", C.c_int32), ("Hkv", C.c_int32),
+                ("d", C.c_int32), ("dt", C.c_int)]
+
+
+class PagedAttnDesc(C.Structure):
+    _fields_ = [("Hq", C.c_int32), ("scale", C.c_float), ("band_bias", C.c_float),
+                ("band_width", C.c_int32), ("window", C.c_int32), ("len_add", C.c_int32)]
 
 
 class MapflowError(RuntimeError):
@@ -100,6 +124,14 @@ def load_library(path: str = LIB_PATH):
         "mf_mapped_av_range": (C.c_int, [P, P, I32, P, P, P, I64, I64, P, SZ, P]),
         "mf_block_stats_noalloc_max_workspace": (SZ, []),
         "mf_block_stats_noalloc": (C.c_int, [P, P, P, P, P, P]),
+        "mf_rope_freqs": (C.c_int, [I32, C.c_double, C.c_int, C.c_double, C.c_double, C.c_double,
+                                    C.c_double, P]),
+        "mf_rope_phases": (C.c_int, [P, I32, P]),
+        "mf_rope": (C.c_int, [P, P, I32, C.c_int, I32, P, I64, P, I64, I32, P, I64, P, I64, I32,
+                              P]),
+        "mf_kv_append": (C.c_int, [P, P, P, P, I64, P, I64, I32, P, I64, P, I64, P]),
+        "mf_paged_attn_workspace": (SZ, [P, P]),
+        "mf_paged_attn": (C.c_int, [P, P, P, P, I64, P, I64, P, P, SZ, P]),
         "mf_mapped_av_plan": (C.c_int, [I32, I32, I32, P]),
         "mf_path_info": (C.c_int, [P, I32, P, P]),
         "mf_exp2_fma_eval": (C.c_int, [P, P, I64, P]),
@@ -394,6 +426,223 @@ def mapped_av(cache: Cache, Hr, W, V, Hkv, page_table=None, page_size=16, O=None
                                     C.c_void_p(wsp), nbytes, _stream()))
     cache._av_ws = ws  # keep the workspace alive until the stream has used it
     return O
+
+
+# ---- the receiver's own tokens: rotary positions, paged keys and values, and
+# the attention of one new token over them
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def _require(ok, msg):
+    if not ok:
+        raise MapflowError(MF_ERR_INVALID_ARG, msg)
+
+
+def _rows(name, t, ntok, H, d, dtype):
+    """Checks a [ntok, H, d] tensor whose heads are d apart; elements between tokens."""
+    _require(t.dim() == 3 and t.shape[0] == ntok and t.shape[1] == H and t.shape[2] == d,
+             f"{name} must be [{ntok}, {H}, {d}], got {tuple(t.shape)}")
+    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
+    st = t.stride()
+    _require(st[2] == 1 and (st[1] == d or H == 1), f"{name}'s heads must be {d} elements apart")
+    return st[0] if ntok > 1 else H * d
+
+
+def _index(name, t, n):
+    _require(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
+             f"{name} must be a contiguous int32 tensor of {n} entries")
+
+
+def _call(device, tensors, f, *args):
+    """f(*args, stream) on the current stream of the tensors' device."""
+    for t in tensors:
+        _require(t is None or (t.is_cuda and t.device == device),
+                 "every tensor must be on one CUDA device")
+    if torch.cuda.current_device() == device.index:
+        _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0.0, low=1.0,
+               high=32.0):
+    """Inverse frequencies float64 [rot_dim/2] (host); scalings as mf_rope_scaling in
+    the C header: "none", "linear", "ntk" or "parts"."""
+    _require(scaling in _SCALINGS, f"scaling must be one of {sorted(_SCALINGS)}")
+    out = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    _check(load_library().mf_rope_freqs(int(rot_dim), base, _SCALINGS[scaling], factor,
+                                        original_length, low, high, out.ctypes.data))
+    return out
+
+
+class Rope:
+    """Rotary positions: the phases of rot_dim/2 pairs (int64 tensor on the device,
+    the bits of mf_rope_phases), their layout and their scale."""
+
+    def __init__(self, phases, interleaved=False, scale=1.0):
+        _require(phases.dtype == torch.int64 and phases.dim() == 1 and phases.is_contiguous(),
+                 "phases must be a contiguous int64 tensor [rot_dim / 2]")
+        self.phases, self.interleaved, self.scale = phases, bool(interleaved), float(scale)
+        self._desc = RopeDesc(2 * phases.shape[0], int(self.interleaved), phases.data_ptr(),
+                              self.scale)
+
+    @classmethod
+    def from_freqs(cls, inv_freq, interleaved=False, scale=1.0, device="cuda"):
+        """From host inverse frequencies (radians per position)."""
+        f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        ph = np.zeros(len(f), dtype=np.uint64)
+        _check(load_library().mf_rope_phases(f.ctypes.data, len(f), ph.ctypes.data))
+        return cls(torch.from_numpy(ph.view(np.int64)).to(device), interleaved, scale)
+
+    @classmethod
+    def make(cls, rot_dim, base=10000.0, interleaved=False, scale=1.0, scaling="none",
+             factor=1.0, original_length=0.0, low=1.0, high=32.0, device="cuda"):
+        return cls.from_freqs(rope_freqs(rot_dim, base, scaling, factor, original_length, low,
+                                         high), interleaved, scale, device)
+
+
+def _batch(ntok, start, cu_seqlens):
+    nseq = ntok if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if cu_seqlens is not None:
+        _index("cu_seqlens", cu_seqlens, nseq + 1)
+    if start is not None:
+        _index("start", start, nseq)
+    return TokenBatch(ntok, nseq, None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                      None if start is None else start.data_ptr())
+
+
+def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=None,
+         backward=False):
+    """Rotates Q [ntok, Hq, d] and, if given, K [ntok, Hk, d]: Q_out, or (Q_out, K_out).
+
+    Token t of sequence s (cu_seqlens [nseq + 1], int32 on the device) has position
+    start[s] + t - cu_seqlens[s]; without cu_seqlens, start [ntok] holds every token's
+    own position.  backward=True takes gradients of the outputs to those of the inputs.
+    Q_out may be Q, and K_out may be K."""
+    _require(start is not None or cu_seqlens is not None, "start or cu_seqlens must be given")
+    _require(Q.dim() == 3, "Q must be [ntok, Hq, d]")
+    ntok, Hq, d = Q.shape
+    dt = Q.dtype
+    b = _batch(ntok, start, cu_seqlens)
+    qs = _rows("Q", Q, ntok, Hq, d, dt)
+    if Q_out is None:
+        Q_out = torch.empty((ntok, Hq, d), dtype=dt, device=Q.device)
+    qos = _rows("Q_out", Q_out, ntok, Hq, d, dt)
+    kargs = (0, None, 0, None, 0)
+    if K is not None:
+        _require(K.dim() == 3 and K.shape[1] > 0, "K must be [ntok, Hk, d]")
+        Hk = K.shape[1]
+        ks = _rows("K", K, ntok, Hk, d, dt)
+        if K_out is None:
+            K_out = torch.empty((ntok, Hk, d), dtype=dt, device=Q.device)
+        kos = _rows("K_out", K_out, ntok, Hk, d, dt)
+        kargs = (Hk, K.data_ptr(), ks, K_out.data_ptr(), kos)
+    else:
+        _require(K_out is None, "K_out without K")
+    _call(Q.device, (Q, K, Q_out, K_out, start, cu_seqlens, rp.phases), load_library().mf_rope,
+          C.byref(rp._desc), C.byref(b), d, _dtype_code(dt), Hq, Q.data_ptr(), qs,
+          Q_out.data_ptr(), qos, *kargs, int(bool(backward)))
+    return Q_out if K is None else (Q_out, K_out)
+
+
+class KVCache:
+    """A receiver's paged keys and values: pools [npages, page_size, Hkv, d] and the page
+    table int32 [nseq, max_pages_per_seq], all owned by the caller.  `V` with `page_table`
+    is what mapped_av reads."""
+
+    def __init__(self, K, V, page_table):
+        _require(K.dim() == 4 and K.shape == V.shape and K.dtype == V.dtype
+                 and K.is_contiguous() and V.is_contiguous(),
+                 "K and V must be contiguous pools [npages, page_size, Hkv, d] of one dtype")
+        _require(page_table.dtype == torch.int32 and page_table.dim() == 2
+                 and page_table.is_contiguous(),
+                 "page_table must be a contiguous int32 tensor [nseq, max_pages_per_seq]")
+        self.K, self.V, self.page_table = K, V, page_table
+        self.npages, self.page_size, self.Hkv, self.d = K.shape
+        self.nseq, self.max_pages = page_table.shape
+        self._desc = KvCacheDesc(K.data_ptr(), V.data_ptr(), page_table.data_ptr(), self.npages,
+                                 self.page_size, self.max_pages, self.nseq, self.Hkv, self.d,
+                                 _dtype_code(K.dtype))
+
+    @classmethod
+    def make(cls, npages, page_size, Hkv, d, dtype, page_table):
+        """New pools (uninitialised) beside a page table."""
+        shape, dev = (int(npages), int(page_size), int(Hkv), int(d)), page_table.device
+        return cls(torch.empty(shape, dtype=dtype, device=dev),
+                   torch.empty(shape, dtype=dtype, device=dev), page_table)
+
+
+def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu_seqlens=None):
+    """Writes new keys (rotated by `rope`, a Rope, if given) and values [ntok, Hkv, d] into
+    their pages, behind the lens[s] tokens (int32 on the device; None: 0) that sequence s
+    holds; rotates the same tokens' queries Q [ntok, Hq, d] and returns them (None
+    without Q).  cu_seqlens [nseq + 1]: the new tokens of every sequence; None: one each.
+    A negative length marks a padding sequence, whose rows are left as they were.
+    `lens` itself is not changed."""
+    _require(K.dim() == 3, "K must be [ntok, Hkv, d]")
+    ntok, dt, d = K.shape[0], cache.K.dtype, cache.d
+    b = _batch(ntok, lens, cu_seqlens)
+    ks = _rows("K", K, ntok, cache.Hkv, d, dt)
+    vs = _rows("V", V, ntok, cache.Hkv, d, dt)
+    qargs = (0, None, 0, None, 0)
+    if Q is not None:
+        _require(Q.dim() == 3 and Q.shape[1] > 0, "Q must be [ntok, Hq, d]")
+        Hq = Q.shape[1]
+        qs = _rows("Q", Q, ntok, Hq, d, dt)
+        if Q_out is None:
+            Q_out = torch.empty((ntok, Hq, d), dtype=dt, device=Q.device)
+        qargs = (Hq, Q.data_ptr(), qs, Q_out.data_ptr(), _rows("Q_out", Q_out, ntok, Hq, d, dt))
+    else:
+        _require(Q_out is None, "Q_out without Q")
+    _call(cache.K.device, (cache.V, cache.page_table, K, V, lens, Q, Q_out, cu_seqlens,
+                           None if rope is None else rope.phases),
+          load_library().mf_kv_append, C.byref(cache._desc),
+          None if rope is None else C.byref(rope._desc), C.byref(b), K.data_ptr(), ks,
+          V.data_ptr(), vs, *qargs)
+    return Q_out
+
+
+def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, band_width=0,
+               window=0, O=None, lse=None, workspace=None):
+    """Attention of one new token per sequence, Q [nseq, Hq, d], over the lens[s] + len_add
+    tokens (int32 on the device) that sequence s holds in `cache`, the new one among them:
+    O [nseq, Hq, d] and the log-sum-exp [Hq, nseq] float32.
+
+    scale: 1/sqrt(d) by default; band_bias within band_width tokens, as the sender's
+    logits; window: keys more than window - 1 tokens back are masked (0: none).
+    `workspace` may be a uint8 device tensor reused across calls (one per call in flight)."""
+    L = load_library()
+    nseq, d, dt = cache.nseq, cache.d, cache.K.dtype
+    _require(Q.dim() == 3, "Q must be [nseq, Hq, d]")
+    Hq = Q.shape[1]
+    qs = _rows("Q", Q, nseq, Hq, d, dt)
+    _index("lens", lens, nseq)
+    dev = Q.device
+    if O is None:
+        O = torch.empty((nseq, Hq, d), dtype=dt, device=dev)
+    os_ = _rows("O", O, nseq, Hq, d, dt)
+    if lse is None:
+        lse = torch.empty((Hq, nseq), dtype=torch.float32, device=dev)
+    _require(lse.dtype == torch.float32 and tuple(lse.shape) == (Hq, nseq)
+             and lse.is_contiguous(), "lse must be a contiguous float32 tensor [Hq, nseq]")
+    a = PagedAttnDesc(Hq, d ** -0.5 if scale is None else scale, band_bias, band_width, window,
+                      len_add)
+    cr, ar = C.byref(cache._desc), C.byref(a)
+    nbytes = L.mf_paged_attn_workspace(cr, ar)
+    if nbytes == 0:  # the call finds the same error and returns its status
+        _check(L.mf_paged_attn(cr, ar, None, None, 0, None, 0, None, None, 0, None))
+    if workspace is not None and workspace.numel() >= nbytes + 256:
+        _require(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+                 "workspace must be a contiguous uint8 tensor")
+        wsp = workspace.data_ptr() + (-workspace.data_ptr()) % 256
+    else:
+        workspace, wsp = _workspace(nbytes, dev)
+    _call(dev, (cache.K, cache.V, cache.page_table, Q, O, lens, lse, workspace),
+          L.mf_paged_attn, cr, ar, lens.data_ptr(), Q.data_ptr(), qs, O.data_ptr(), os_,
+          lse.data_ptr(), wsp, nbytes)
+    return O, lse
 
 
 def mapped_av_plan(Hs, Hr, Hkv):

@@ -326,6 +326,159 @@ mf_status mf_cache_offload(const mf_csr_cache* dev_src, mf_csr_cache* host_dst,
 mf_status mf_cache_fetch(const mf_csr_cache* host_src, mf_csr_cache* dev_dst, int64_t qb_begin,
                          int64_t qb_end, mf_stream_t stream);
 
+/* ---- the receiver's own tokens: rotary positions, a paged key-value cache,
+ * and the attention of one new token over it.  The mapped prefill above gives
+ * O for a shared context from the sender's map and the receiver's V; the
+ * tokens that follow are the receiver's own (article: the receiver keeps its
+ * own V; PagedAttention is supported).  Their keys and values go to page pools
+ * -- the V pool is the one mf_v_desc reads -- and every new token attends to
+ * all of them.  These calls find sequence lengths on the device, so a decode
+ * loop needs no host round trip and can be captured into a CUDA graph; make
+ * the first call on a device before a capture (it looks up the status word's
+ * address).  None of them allocates. */
+
+/* Rotary positions.  Pair i of a head (i < rot_dim / 2) turns by the angle
+ * position * f_i, and is multiplied by `scale`:
+ *   y[a] = scale (x[a] cos - x[b] sin),  y[b] = scale (x[a] sin + x[b] cos),
+ * with (a, b) = (i, i + rot_dim/2), or (2i, 2i + 1) if interleaved is not 0.
+ * Dims rot_dim .. d-1 are copied.  rot_dim: even, 2 .. d.
+ *  phases: device [rot_dim/2], f_i as 2^64 f_i / (2 pi) modulo 2^64
+ *          (mf_rope_phases): position * phase wraps to whole turns exactly,
+ *          so far positions lose no digits.
+ * Arithmetic is float32; each output is rounded once to its dtype. */
+typedef struct {
+  int32_t rot_dim;
+  int32_t interleaved;
+  const uint64_t* phases;
+  float scale;
+} mf_rope_desc;
+
+/* How mf_rope_freqs scales base^(-2i/rot_dim) for contexts `factor` times as
+ * long as the original:
+ *  NONE    f_i = base^(-2i/rot_dim);
+ *  LINEAR  f_i / factor (position interpolation);
+ *  NTK     base' = base * factor^(rot_dim / (rot_dim - 2)) (rot_dim > 2);
+ *  PARTS   by the turns n_i = original_length f_i / (2 pi) a pair makes in the
+ *          original context: g = clamp((n_i - low) / (high - low), 0, 1),
+ *          f_i' = (1 - g) f_i / factor + g f_i (the "NTK-by-parts" of the YaRN
+ *          paper, arXiv 2309.00071; its attention factor goes into `scale`). */
+typedef enum {
+  MF_ROPE_NONE = 0,
+  MF_ROPE_LINEAR = 1,
+  MF_ROPE_NTK = 2,
+  MF_ROPE_PARTS = 3
+} mf_rope_scaling;
+
+/* Inverse frequencies f_i [rot_dim/2] (host, out), in radians per position.
+ * Host only.  Errors: MF_ERR_INVALID_ARG (rot_dim odd or < 2, base <= 0,
+ * factor <= 0 where it is used, PARTS without original_length > 0 or with
+ * high <= low, an unknown kind, NULL). */
+mf_status mf_rope_freqs(int32_t rot_dim, double base, mf_rope_scaling kind, double factor,
+                        double original_length, double low, double high, double* inv_freq);
+
+/* Phases [n] (host, out) of the inverse frequencies [n] (host); copy them to
+ * the device for mf_rope_desc.  Errors: MF_ERR_INVALID_ARG (n < 0, NULL, a
+ * frequency that is not finite). */
+mf_status mf_rope_phases(const double* inv_freq, int32_t n, uint64_t* phases);
+
+/* The tokens of a call: ntok packed tokens of nseq sequences.
+ *  cu_seqlens: device [nseq+1], prefix sums of the tokens per sequence in this
+ *              call, from 0 to ntok; NULL: one token per sequence (ntok = nseq).
+ *  start:      device [nseq], the position of each sequence's first token in
+ *              this call; NULL: 0.
+ * Token t of sequence s has position start[s] + t - cu_seqlens[s].  With
+ * cu_seqlens NULL, `start` is every token's own position. */
+typedef struct {
+  int64_t ntok;
+  int32_t nseq;
+  const int32_t* cu_seqlens;
+  const int32_t* start;
+} mf_token_batch;
+
+/* Rotates Q [ntok][Hq][d] into Q_out and K [ntok][Hk][d] into K_out (the
+ * inputs mf_block_stats takes, or a receiver's own).  The strides are elements
+ * between tokens (>= H d), so slices of a fused projection work; heads are
+ * d apart.  An output may be its input (same pointer and stride), but must
+ * not overlap it otherwise.  Hk = 0: no K (K and K_out may be NULL).
+ *  backward: 0, or 1 for the transposed map, which takes the gradients of
+ *            Q_out and K_out to those of Q and K.
+ * d: 64 or 128; pointers aligned to their element.  Positions may be negative.
+ * Errors: MF_ERR_INVALID_ARG, MF_ERR_UNSUPPORTED (d), MF_ERR_CUDA. */
+mf_status mf_rope(const mf_rope_desc* rope, const mf_token_batch* batch, int32_t d, mf_dtype dt,
+                  int32_t Hq, const void* Q, int64_t q_stride, void* Q_out, int64_t qo_stride,
+                  int32_t Hk, const void* K, int64_t k_stride, void* K_out, int64_t ko_stride,
+                  int32_t backward, mf_stream_t stream);
+
+/* A receiver's paged keys and values (caller-owned device memory).
+ *  K, V: pools [npages][page_size][Hkv][d] of dtype dt, 16-byte aligned.
+ *  page_table: device [nseq][max_pages_per_seq]; entry (s, p) is the pool page
+ *          of tokens p*page_size .. of sequence s.  Entries of pages that hold
+ *          no token are never read.  Sequences may share pages (a shared
+ *          prefix), as long as no call writes one.
+ *  page_size: a multiple of 16, as in mf_v_desc.  d: 64 or 128. */
+typedef struct {
+  void* K;
+  void* V;
+  const int32_t* page_table;
+  int64_t npages;
+  int32_t page_size;
+  int32_t max_pages_per_seq;
+  int32_t nseq, Hkv, d;
+  mf_dtype dt;
+} mf_kv_cache;
+
+/* Writes the new keys and values of a batch into their pages, the keys rotated
+ * on the way, and (Hq > 0) rotates the same tokens' queries: prompts, chunks
+ * behind a cached prefix, or one token per sequence.
+ *  batch->start: tokens each sequence already holds (NULL: none), so its new
+ *          tokens take the positions behind them; batch->nseq = cache->nseq.
+ *          A negative entry marks a padding sequence: its tokens' rows of the
+ *          pools and of Q_out are left as they were.
+ *  K, V [ntok][Hkv][d], Q and Q_out [ntok][Hq][d], strides as in mf_rope;
+ *  Q_out may be Q.  rope NULL: K and Q are copied unrotated.
+ * A token whose page lies beyond max_pages_per_seq or whose table entry is
+ * outside [0, npages) is not written and sets the device status
+ * (MF_ERR_INVALID_ARG via mf_sync_status).  Two tokens must not share a slot.
+ * Errors: MF_ERR_INVALID_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA. */
+mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
+                       const mf_token_batch* batch, const void* K, int64_t k_stride,
+                       const void* V, int64_t v_stride, int32_t Hq, const void* Q,
+                       int64_t q_stride, void* Q_out, int64_t qo_stride, mf_stream_t stream);
+
+/* Attention of one new token per sequence over the paged cache.  Sequence s
+ * holds L = lens[s] + len_add tokens, the new one (position L - 1) among them:
+ *   x_j = scale q.k_j + band_bias [L-1-j < band_width],  j < L, L-1-j < window
+ *   O = sum_j softmax(x)_j v_j,  lse = log sum_j exp x_j
+ * (the band of mf_attn_desc; window 0: no limit).  Query head h reads KV head
+ * floor(h Hkv / Hq).
+ *  lens: device [nseq].  A sequence with L <= 0 gets O = 0 and lse = -inf.
+ *  Q [nseq][Hq][d] and O [nseq][Hq][d] of the cache's dtype, 16-byte aligned,
+ *  strides (elements between sequences) multiples of 16 bytes; O may be Q.
+ *  lse [Hq][nseq] float, or NULL.
+ * Softmax statistics and sums are float32.  A key whose page is outside the
+ * pool or the table counts as masked and sets the device status
+ * (MF_ERR_INVALID_ARG via mf_sync_status).  Rows of the pools past a
+ * sequence's end, and keys outside the window, have no influence, whatever
+ * they hold.  Results do not depend on scheduling.
+ *  ws: at least mf_paged_attn_workspace(cache, attn) bytes (device, 256-byte
+ *  aligned); calls that may overlap need a workspace each.
+ * Hq: a multiple of Hkv, at most 256.  Errors: MF_ERR_INVALID_ARG,
+ * MF_ERR_UNSUPPORTED, MF_ERR_WORKSPACE, MF_ERR_CUDA. */
+typedef struct {
+  int32_t Hq;
+  float scale;
+  float band_bias;
+  int32_t band_width;
+  int32_t window;
+  int32_t len_add;
+} mf_paged_attn_desc;
+
+size_t mf_paged_attn_workspace(const mf_kv_cache* cache, const mf_paged_attn_desc* attn);
+mf_status mf_paged_attn(const mf_kv_cache* cache, const mf_paged_attn_desc* attn,
+                        const int32_t* lens, const void* Q, int64_t q_stride, void* O,
+                        int64_t o_stride, float* lse, void* ws, size_t ws_bytes,
+                        mf_stream_t stream);
+
 /* Diagnostic, not on the hot path: y[i] = 2^x[i] by the FMA-pipe
  * exponential of the block-statistics kernel, which computes 2 of every 8 of
  * its exponentials this way (the rest on MUFU): x = j + f, j = round(x); 2^f
@@ -375,7 +528,8 @@ mf_status mf_selftest_timeout(int32_t limit_ms, mf_stream_t stream);
  * current device: MF_OK; MF_ERR_TIMEOUT (a bounded wait gave up);
  * MF_ERR_CAPACITY (kept blocks overflowed a CSR capacity); MF_ERR_INVALID_ARG
  * (the fused kernel met a cache row holding more entries than its query block
- * has key blocks, and clamped it). */
+ * has key blocks, and clamped it; or a token's place in a paged key-value cache
+ * lay outside its table or pool, and was skipped). */
 mf_status mf_sync_status(mf_stream_t stream);
 
 /* ---- host-side prefix index (article: states are indexed by a prefix hash
