@@ -26,6 +26,7 @@
 //    in shared memory when a whole block works on one row, and a second,
 //    dependent launch joins them.  The cuts and the order of the sums depend
 //    on the lengths alone.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -54,6 +55,7 @@ struct Params {
   int64_t q_stride, o_stride, npages;
   int nseq, Hq, Hkv, G, page_size, max_pages, len_add, band, window;
   int groups, gh;  // groups of query heads per KV head, heads of a group
+  int min_run;     // units of a run, if there are fewer than that for every warp
   float scale2, bias2;  // times log2 e
   // workspace: pieces of cut rows (two per warp: the row its run begins in,
   // the row it ends in), where the runs begin, the number of units
@@ -86,9 +88,30 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
   return k;
 }
 
-// Unit where warp w's run begins, of `total` cut into `warps` runs.
-__device__ __forceinline__ int64_t cut(int64_t total, int w, int warps) {
-  return total * w / warps;
+// The line of units cut into kCtas << shift equal runs, 1 << shift per block.
+struct Cuts {
+  int64_t total;
+  int shift;
+  // first unit of run w
+  __device__ __forceinline__ int64_t at(int w) const {
+    const uint64_t x = uint64_t(total) * uint32_t(w);
+    return int64_t((x >> 32 ? x / kCtas : uint32_t(x) / uint32_t(kCtas)) >> shift);
+  }
+  // the run that holds unit u
+  __device__ __forceinline__ int holder(int64_t u) const {
+    const uint64_t x = uint64_t(u + 1) * uint32_t(kCtas << shift) - 1;
+    return x >> 32 ? int(x / uint64_t(total)) : int(uint32_t(x) / uint32_t(total));
+  }
+};
+
+// Runs shorter than this cost more in pieces to join than they save: a piece
+// (gh rows of float32, written and read once) is gh / 4 of a unit's bytes in
+// bf16, half that in float32.
+template <int WARPS>
+__device__ __forceinline__ Cuts cuts_of(const Params& p, int64_t total) {
+  int shift = WARPS == 8 ? 3 : 2;
+  while (shift > 0 && total < (int64_t(kCtas) << shift) * p.min_run) --shift;
+  return Cuts{total, shift};
 }
 
 // A place in the line of units.
@@ -141,15 +164,17 @@ __device__ __forceinline__ void plan_units(const Params& p, PlanSmem<THREADS>& s
   __syncthreads();
 }
 
-// The place of unit u < before[THREADS].
+// The place of unit u < before[THREADS] (the same u in the whole warp).
 template <int THREADS>
 __device__ __forceinline__ Walk find_unit(const Params& p, const PlanSmem<THREADS>& sm,
                                           int64_t u) {
-  const int per = (p.nseq + THREADS - 1) / THREADS;
-  const int t = upper_index(sm.before, THREADS, u);
+  constexpr int kSub = THREADS / 32;
+  const int lane = threadIdx.x % 32;
+  const int t0 = (__popc(__ballot_sync(0xffffffffu, sm.before[lane * kSub] <= u)) - 1) * kSub;
+  const int t = t0 - 1 + __popc(__ballot_sync(0xffffffffu, lane < kSub && sm.before[t0 + lane % kSub] <= u));
   int64_t at = u - sm.before[t];
   Walk w;
-  w.s = t * per;
+  w.s = t * ((p.nseq + THREADS - 1) / THREADS);
   const int rows = p.Hkv * p.groups;
   while (true) {
     w.k = span_of(p, w.s);
@@ -158,8 +183,8 @@ __device__ __forceinline__ Walk find_unit(const Params& p, const PlanSmem<THREAD
     at -= n;
     ++w.s;
   }
-  w.r = int(at / w.k.n);
-  w.g = int(at % w.k.n);
+  w.r = at >> 32 ? int(at / w.k.n) : int(uint32_t(at) / uint32_t(w.k.n));
+  w.g = int(at - int64_t(w.r) * w.k.n);
   return w;
 }
 
@@ -376,18 +401,19 @@ struct Bf16Body {
           }
       }
   }
-  // f(head, dim, O[dim], O[dim + 1], m, l), every pair once over the warp.
-  template <typename F>
-  __device__ __forceinline__ void each(int heads, F f) const {
+  // Hands every row to `sink`, pair of dims by pair of dims.
+  template <class Sink>
+  __device__ __forceinline__ void put(int heads, const Sink& sink) const {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int n = 0; n < NR; ++n)
-        if (row(b, n) < heads)
+        if (row(b, n) < heads) {
+          const auto to = sink.row(row(b, n), m[b][n], l[b][n], lane % 4 == 0);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
-            f(row(b, n), i * 8 + 2 * (lane % 4), o[b][i][2 * n], o[b][i][2 * n + 1], m[b][n],
-              l[b][n]);
+            to.store(i * 8 + 2 * (lane % 4), o[b][i][2 * n], o[b][i][2 * n + 1]);
+        }
   }
 };
 
@@ -541,14 +567,15 @@ struct F32Body {
     }
     __syncwarp();
   }
-  template <typename F>
-  __device__ __forceinline__ void each(int heads, F f) const {
+  template <class Sink>
+  __device__ __forceinline__ void put(int heads, const Sink& sink) const {
 #pragma unroll
     for (int g = 0; g < GT; ++g)
-      if (g < heads)
+      if (g < heads) {
+        const auto to = sink.row(g, cs[g], ws[g], lane == 0);
 #pragma unroll
-        for (int n = 0; n < NO / 2; ++n)
-          f(g, lane * NO + 2 * n, o[g][n].x, o[g][n].y, cs[g], ws[g]);
+        for (int n = 0; n < NO / 2; ++n) to.store(lane * NO + 2 * n, o[g][n].x, o[g][n].y);
+      }
   }
 };
 
@@ -561,29 +588,48 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
   *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
 }
 
-// Where one row's result goes: its O and lse, or (slot >= 0) a piece.
+// A finished row: O and lse of query heads h0 .. of sequence s.
 template <typename T, int D>
-struct Sink {
+struct Finished {
   const Params& p;
-  int s, h0;  // sequence, first query head
-  int64_t slot;
-  __device__ __forceinline__ void put(int head, int dim, float a, float b, float m,
-                                      float l) const {
-    if (slot >= 0) {
-      store2(p.part_o + (slot * p.gh + head) * D + dim, a, b);
-      if (dim == 0) p.part_ml[slot * p.gh + head] = make_float2(m, l);
-      return;
+  int s, h0;
+  struct To {
+    T* o;
+    float inv;
+    bool none;  // nothing seen: zero, whatever was summed
+    __device__ __forceinline__ void store(int dim, float a, float b) const {
+      store2(o + dim, none ? 0.f : a * inv, none ? 0.f : b * inv);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T* o = static_cast<T*>(p.O) + s * p.o_stride + int64_t(h0 + head) * D + dim;
-    if (l == 0.f)
-      store2(o, 0.f, 0.f);
-    else
-      store2(o, a * inv, b * inv);
-    if (dim == 0 && p.lse)
-      p.lse[int64_t(h0 + head) * p.nseq + s] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  };
+  __device__ __forceinline__ To row(int head, float m, float l, bool first) const {
+    const bool none = l == 0.f;
+    if (first && p.lse)
+      p.lse[int64_t(h0 + head) * p.nseq + s] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    return To{static_cast<T*>(p.O) + s * p.o_stride + int64_t(h0 + head) * D, 1.f / l, none};
   }
 };
+
+// A piece of a row: unnormalised sums [heads][D], maxima and sums of weights.
+template <int D>
+struct PieceAt {
+  float* o;
+  float2* ml;
+  struct To {
+    float* o;
+    __device__ __forceinline__ void store(int dim, float a, float b) const {
+      store2(o + dim, a, b);
+    }
+  };
+  __device__ __forceinline__ To row(int head, float m, float l, bool first) const {
+    if (first) ml[head] = make_float2(m, l);
+    return To{o + head * D};
+  }
+};
+
+template <int D>
+__device__ __forceinline__ PieceAt<D> piece_at(const Params& p, int64_t slot) {
+  return PieceAt<D>{p.part_o + slot * p.gh * D, p.part_ml + slot * p.gh};
+}
 
 // ------------------------------------------------------------ the main kernel
 
@@ -601,7 +647,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   using T = typename Body::T;
   using S = Shared<Body>;
   constexpr int D = Body::D, kWarps = Body::kWarps, kStages = Body::kStages;
-  constexpr int kThreads = kWarps * 32, kAll = kCtas * kWarps;
+  constexpr int kThreads = kWarps * 32;
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PlanSmem<kThreads> plan;
@@ -618,21 +664,26 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }
+  // all before this ran beside the end of the launch before
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   plan_units<kThreads>(p, plan, blockIdx.x == 0);
   // the joining kernel may take its place now; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int64_t total = plan.before[kThreads];
-  const int w = blockIdx.x * kWarps + warp;
-  const int64_t u0 = cut(total, w, kAll), u1 = cut(total, w + 1, kAll);
+  const Cuts cuts = cuts_of<kWarps>(p, plan.before[kThreads]);
+  const int w0 = blockIdx.x << cuts.shift, w = w0 + warp;
+  const int64_t c0 = cuts.at(w0), c1 = cuts.at(w0 + (1 << cuts.shift));
+  int64_t u0 = c1, u1 = c1;
+  if (warp >> cuts.shift == 0) {
+    u0 = cuts.at(w);
+    u1 = cuts.at(w + 1);
+  }
   const int n_units = int(u1 - u0);
   Walk at = {};
   if (n_units > 0) at = find_unit<kThreads>(p, plan, u0);
-  if (lane == 0) p.starts[w] = Start{at.s, at.r, at.g, at.k.n};
-  if (w == 0 && lane == 0) *p.total = total;
+  if (lane == 0 && warp >> cuts.shift == 0) p.starts[w] = Start{at.s, at.r, at.g, at.k.n};
+  if (w == 0 && lane == 0) *p.total = cuts.total;
   // does this block's whole run lie in one row?
-  const int64_t c0 = cut(total, blockIdx.x * kWarps, kAll);
-  const int64_t c1 = cut(total, (blockIdx.x + 1) * kWarps, kAll);
   const bool together =
       __syncthreads_or(n_units > 0 && u0 - at.g <= c0 && u0 - at.g + at.k.n >= c1) != 0;
 
@@ -718,10 +769,10 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     if (!ok) break;
     body.finish();
     if (together) break;  // one row: joined below
-    const Sink<T, D> sink{p, at.s, h0, whole ? -1 : done == run ? 2 * w : 2 * w + 1};
-    body.each(heads, [&](int h, int d, float a, float b, float m, float l) {
-      sink.put(h, d, a, b, m, l);
-    });
+    if (whole)
+      body.put(heads, Finished<T, D>{p, at.s, h0});
+    else
+      body.put(heads, piece_at<D>(p, done == run ? 2 * w : 2 * w + 1));
     at.g += run - 1;
     if (done < n_units) at.step(p);
   }
@@ -741,11 +792,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     const int heads = min(p.gh, p.G - at.r % p.groups * p.gh);
     join_ml[warp][lane] = make_float2(-INFINITY, 0.f);
     __syncwarp();
-    if (n_units > 0 && ok)
-      body.each(heads, [&](int h, int d, float a, float b, float m, float l) {
-        store2(mine + h * D + d, a, b);
-        if (d == 0) join_ml[warp][h] = make_float2(m, l);
-      });
+    if (n_units > 0 && ok) body.put(heads, PieceAt<D>{mine, join_ml[warp]});
     // every block whose run is not empty has a warp whose run is not empty; the
     // row is that of the first such warp
     __shared__ int row_s, row_r;
@@ -758,23 +805,30 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     __syncthreads();
     const int g2 = row_r % p.groups, hh = row_r / p.groups * p.G + g2 * p.gh;
     const int nh = min(p.gh, p.G - g2 * p.gh);
-    const Sink<T, D> sink{p, row_s, hh, row_whole ? -1 : int64_t(2) * blockIdx.x * kWarps};
     for (int i = threadIdx.x; i < nh * (D / 2); i += kThreads) {
       const int h = i / (D / 2), d = i % (D / 2) * 2;
+      float2 ml[kWarps], t[kWarps];
       float m = -INFINITY, l = 0.f, a = 0.f, b = 0.f;
-      for (int v = 0; v < kWarps; ++v) m = fmaxf(m, join_ml[v][h].x);
-      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
       for (int v = 0; v < kWarps; ++v) {
-        const float2 ml = join_ml[v][h];
-        if (ml.y == 0.f) continue;
-        const float c = ex2(ml.x - ref);
-        const float2 t = *reinterpret_cast<const float2*>(
-            smem + v * kStages * S::kStageBytes + (h * D + d) * 4);
-        l = fmaf(ml.y, c, l);
-        a = fmaf(t.x, c, a);
-        b = fmaf(t.y, c, b);
+        ml[v] = join_ml[v][h];
+        t[v] = *reinterpret_cast<const float2*>(smem + v * kStages * S::kStageBytes +
+                                                (h * D + d) * 4);
+        m = fmaxf(m, ml[v].x);
       }
-      sink.put(h, d, a, b, m, l);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float c = ex2(ml[v].x - ref);
+        const bool some = ml[v].y != 0.f;  // else its sums are not there
+        l = fmaf(ml[v].y, c, l);
+        a = fmaf(some ? t[v].x : 0.f, c, a);
+        b = fmaf(some ? t[v].y : 0.f, c, b);
+      }
+      if (row_whole)
+        Finished<T, D>{p, row_s, hh}.row(h, m, l, d == 0).store(d, a, b);
+      else
+        piece_at<D>(p, int64_t(2) * w0).row(h, m, l, d == 0).store(d, a, b);
     }
   }
   // sequences without keys
@@ -792,7 +846,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
 // One warp per cut that is the first inside its row, and a query head
 // (blockIdx.y); a row of many pieces takes the whole block.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinAlone = 64;  // warps' runs a single warp looks through
+constexpr int kJoinAlone = 8;  // runs of a row that one warp joins by itself
 
 template <int D>
 struct Piece {  // running joint result; a lane owns D / 32 dims
@@ -812,44 +866,37 @@ struct Row {
   int v0, v1;    // first and last run that holds one of them
 };
 
-template <int D, int WARPS>  // WARPS of the main kernel's blocks
-__device__ __forceinline__ void join_runs(const Params& p, const Row& row, int64_t total, int head,
-                                          int first, int step, Piece<D>& acc) {
-  constexpr int kAll = kCtas * WARPS;
+template <int D>
+__device__ __forceinline__ void join_runs(const Params& p, const Row& row, const Cuts& cuts,
+                                          int head, int warp, int warps, Piece<D>& acc) {
   const int lane = threadIdx.x % 32;
-  for (int base = row.v0 + first; base <= row.v1; base += step) {
-    const int v = base + lane;
-    int64_t slot = -1;
-    if (v <= row.v1) {
-      const int64_t u0 = cut(total, v, kAll), u1 = cut(total, v + 1, kAll);
-      const int c = v / WARPS;
-      const int64_t c0 = cut(total, c * WARPS, kAll), c1 = cut(total, (c + 1) * WARPS, kAll);
+  // eights of runs go round the warps, so that the pieces of whole blocks do too
+  for (int base = row.v0 & ~7; base <= row.v1; base += 32 * warps) {
+    const int v = base + (lane / 8 * warps + warp) * 8 + lane % 8;
+    int slot = -1;
+    if (v >= row.v0 && v <= row.v1) {
+      const int64_t u0 = cuts.at(v), u1 = cuts.at(v + 1);
+      const int w0 = v >> cuts.shift << cuts.shift;
+      const int64_t c0 = cuts.at(w0), c1 = cuts.at(w0 + (1 << cuts.shift));
       if (u0 < u1) {
-        if (c0 >= row.a && c1 <= row.e)
-          slot = u0 == c0 ? int64_t(2) * c * WARPS : -1;
+        if (c0 >= row.a && c1 <= row.e)  // joined by its block
+          slot = u0 == c0 ? 2 * w0 : -1;
         else
-          slot = u0 >= row.a ? int64_t(2) * v : int64_t(2) * v + 1;
+          slot = u0 >= row.a ? 2 * v : 2 * v + 1;
       }
     }
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (slot >= 0) ml = __ldcg(&p.part_ml[slot * p.gh + head]);
-    if (ml.y == 0.f) slot = -1;  // an empty piece
+    if (slot >= 0) ml = __ldcg(&p.part_ml[int64_t(slot) * p.gh + head]);
     unsigned left = __ballot_sync(0xffffffffu, slot >= 0);
     while (left) {
-      constexpr int kBatch = 4;
-      float o[kBatch][D / 32], m[kBatch], l[kBatch];
+      constexpr int kBatch = 8;
+      float o[kBatch][D / 32];
+      unsigned now = left;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int src = left ? __ffs(left) - 1 : 0;
-        const bool live = left != 0;
-        left &= left - 1;
-        const int64_t at = __shfl_sync(0xffffffffu, slot, src);
-        m[i] = live ? __shfl_sync(0xffffffffu, ml.x, src) : -INFINITY;
-        l[i] = live ? __shfl_sync(0xffffffffu, ml.y, src) : 0.f;
-        const float* x = p.part_o + (at * p.gh + head) * D + lane * (D / 32);
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) o[i][d] = 0.f;
-        if (live) {
+        const int at = __shfl_sync(0xffffffffu, slot, now ? __ffs(now) - 1 : 0);
+        const float* x = p.part_o + (int64_t(at) * p.gh + head) * D + lane * (D / 32);
+        if (now) {
           if (D == 128) {
             const float4 t = __ldcg(reinterpret_cast<const float4*>(x));
             o[i][0] = t.x, o[i][1] = t.y, o[i][D / 32 - 2] = t.z, o[i][D / 32 - 1] = t.w;
@@ -858,9 +905,16 @@ __device__ __forceinline__ void join_runs(const Params& p, const Row& row, int64
             o[i][0] = t.x, o[i][1] = t.y;
           }
         }
+        now &= now - 1;
       }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) acc.add(m[i], l[i], o[i]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int src = left ? __ffs(left) - 1 : 0;
+        const float m = __shfl_sync(0xffffffffu, ml.x, src);
+        const float l = __shfl_sync(0xffffffffu, ml.y, src);
+        if (left && l != 0.f) acc.add(m, l, o[i]);  // l = 0: an empty piece, its sums void
+        left &= left - 1;
+      }
     }
   }
 }
@@ -869,42 +923,42 @@ template <typename T, int D>
 __device__ __forceinline__ void put_row(const Params& p, const Row& row, int head,
                                         const Piece<D>& x) {
   const int group = row.r % p.groups;
-  const Sink<T, D> sink{p, row.s, row.r / p.groups * p.G + group * p.gh, -1};
+  const int lane = threadIdx.x % 32;
+  const Finished<T, D> sink{p, row.s, row.r / p.groups * p.G + group * p.gh};
+  const auto to = sink.row(head, x.m, x.l, lane == 0);
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2)
-    sink.put(head, threadIdx.x % 32 * (D / 32) + i, x.o[i], x.o[i + 1], x.m, x.l);
+  for (int i = 0; i < D / 32; i += 2) to.store(lane * (D / 32) + i, x.o[i], x.o[i + 1]);
 }
 
-template <typename T, int D, int WARPS>
+template <typename T, int D, int WARPS>  // WARPS of the main kernel's blocks
 __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const Params p) {
-  constexpr int kAll = kCtas * WARPS;
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float2 sm_ml[kJoinWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t total = *p.total;
-  if (total == 0) return;
   const int head = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  auto owner = [&](int64_t u) { return int(((u + 1) * kAll - 1) / total); };
+  const int w = blockIdx.x * kJoinWarps + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Start st = lane < kJoinWarps ? p.starts[w] : Start{};
+  const Cuts cuts = cuts_of<WARPS>(p, *p.total);
+  if (blockIdx.x * kJoinWarps >= kCtas << cuts.shift) return;
 
   // lane i: the cut before run blockIdx.x * 8 + i
   Row row = {};
   bool split = false;
-  const int w = blockIdx.x * kJoinWarps + lane;
-  if (lane < kJoinWarps && w > 0) {
-    const int64_t u = cut(total, w, kAll);
-    if (cut(total, w + 1, kAll) > u) {
-      const Start st = p.starts[w];
-      if (st.g > 0) {
-        row = Row{u - st.g, u - st.g + st.n, st.s, st.r, 0, 0};
-        const int group = st.r % p.groups, heads = min(p.gh, p.G - group * p.gh);
-        split = head < heads && row.a >= cut(total, owner(u - 1), kAll);
-        if (split) {
-          row.v0 = owner(row.a);
-          row.v1 = owner(row.e - 1);
-          const int c = row.v0 / WARPS;  // a block that held just this row is done with it
-          if (row.a == cut(total, c * WARPS, kAll) && row.e == cut(total, (c + 1) * WARPS, kAll))
-            split = false;
-        }
+  if (lane < kJoinWarps && w > 0 && w < kCtas << cuts.shift) {
+    const int64_t u = cuts.at(w);
+    const int group = st.r % p.groups, heads = min(p.gh, p.G - group * p.gh);
+    if (cuts.at(w + 1) > u && st.g > 0 && head < heads) {
+      row = Row{u - st.g, u - st.g + st.n, st.s, st.r, 0, 0};
+      // the first cut inside the row: the run before, the last that is not
+      // empty, begins no later than the row
+      const bool full = cuts.total >= kCtas << cuts.shift;
+      split = row.a >= (full ? cuts.at(w - 1) : u - 1);
+      if (split) {
+        row.v0 = full ? w - 1 : cuts.holder(row.a);
+        row.v1 = cuts.holder(row.e - 1);
+        const int w0 = row.v0 >> cuts.shift << cuts.shift;
+        // a block that held just this row is done with it
+        if (row.a == cuts.at(w0) && row.e == cuts.at(w0 + (1 << cuts.shift))) split = false;
       }
     }
   }
@@ -923,14 +977,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const Params p) 
   if ((mine >> warp) & 1) {
     const Row x = row_of(warp);
     Piece<D> acc;
-    join_runs<D, WARPS>(p, x, total, head, 0, 32, acc);
+    join_runs<D>(p, x, cuts, head, 0, 1, acc);
     put_row<T, D>(p, x, head, acc);
   }
   while (shared) {  // the same in every warp
     const Row x = row_of(__ffs(shared) - 1);
     shared &= shared - 1;
     Piece<D> acc;
-    join_runs<D, WARPS>(p, x, total, head, warp * 32, kJoinWarps * 32, acc);
+    join_runs<D>(p, x, cuts, head, warp, kJoinWarps, acc);
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) sm_o[warp][lane * (D / 32) + d] = acc.o[d];
@@ -991,6 +1045,7 @@ size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   if (p) {
     p->groups = groups;
     p->gh = gh;
+    p->min_run = std::max(1, gh / (c.dt == MF_BF16 ? 8 : 16));
     p->part_o = part_o;
     p->part_ml = part_ml;
     p->starts = starts;
@@ -1006,18 +1061,22 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   cudaError_t e = cudaFuncSetAttribute(k_paged_attn<Body>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  k_paged_attn<Body><<<kCtas, Body::kWarps * 32, kSmem, st>>>(tk, tv, p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // either launch may take its place before the one ahead of it has ended
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas * Body::kWarps / kJoinWarps, p.gh);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(Body::kWarps * 32);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k_paged_attn<Body>, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((kCtas * Body::kWarps + kJoinWarps - 1) / kJoinWarps, p.gh);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_paged_join<typename Body::T, Body::D, Body::kWarps>, p);
 }
 
