@@ -27,6 +27,7 @@
 //    dependent launch joins them.  The cuts and the order of the sums depend
 //    on the lengths alone.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -1058,9 +1059,18 @@ template <class Body>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv,
                    cudaStream_t st) {
   constexpr int kSmem = Shared<Body>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(k_paged_attn<Body>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // once per device: the call costs as much as a fifth of a launch
+  static std::atomic<uint64_t> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);  // status_word() refuses devices past 63
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_paged_attn<Body>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   // either launch may take its place before the one ahead of it has ended
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -434,36 +434,51 @@ def mapped_av(cache: Cache, Hr, W, V, Hkv, page_table=None, page_size=16, O=None
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
+def _refuse(msg):
+    raise MapflowError(MF_ERR_INVALID_ARG, msg)
+
+
 def _require(ok, msg):
     if not ok:
-        raise MapflowError(MF_ERR_INVALID_ARG, msg)
+        _refuse(msg)
 
+
+# The checks below run in every call of a decode step: messages are put together
+# only where one is refused.
 
 def _rows(name, t, ntok, H, d, dtype):
     """Checks a [ntok, H, d] tensor whose heads are d apart; elements between tokens."""
-    _require(t.dim() == 3 and t.shape[0] == ntok and t.shape[1] == H and t.shape[2] == d,
-             f"{name} must be [{ntok}, {H}, {d}], got {tuple(t.shape)}")
-    _require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    st = t.stride()
-    _require(st[2] == 1 and (st[1] == d or H == 1), f"{name}'s heads must be {d} elements apart")
-    return st[0] if ntok > 1 else H * d
+    if t.shape != (ntok, H, d):
+        _refuse(f"{name} must be [{ntok}, {H}, {d}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        _refuse(f"{name} must be {dtype}, got {t.dtype}")
+    token, head, dim = t.stride()
+    if dim != 1 or (head != d and H != 1):
+        _refuse(f"{name}'s heads must be {d} elements apart")
+    return token if ntok > 1 else H * d
 
 
 def _index(name, t, n):
-    _require(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-             f"{name} must be a contiguous int32 tensor of {n} entries")
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 tensor of {n} entries")
+
+
+def _new_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _call(device, tensors, f, *args):
-    """f(*args, stream) on the current stream of the tensors' device."""
+    """f(*args, stream) on the current stream of the tensors' device (its index)."""
     for t in tensors:
-        _require(t is None or (t.is_cuda and t.device == device),
-                 "every tensor must be on one CUDA device")
-    if torch.cuda.current_device() == device.index:
-        _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+        if t is not None and t.get_device() != device or device < 0:
+            _refuse("every tensor must be on one CUDA device")
+    # the raw handles: torch.cuda's objects around them cost as much as a launch
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        _check(f(*args, stream))
     else:
         with torch.cuda.device(device):
-            _check(f(*args, torch.cuda.current_stream(device).cuda_stream))
+            _check(f(*args, stream))
 
 
 def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0.0, low=1.0,
@@ -528,7 +543,7 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     b = _batch(ntok, start, cu_seqlens)
     qs = _rows("Q", Q, ntok, Hq, d, dt)
     if Q_out is None:
-        Q_out = torch.empty((ntok, Hq, d), dtype=dt, device=Q.device)
+        Q_out = _new_like(Q)
     qos = _rows("Q_out", Q_out, ntok, Hq, d, dt)
     kargs = (0, None, 0, None, 0)
     if K is not None:
@@ -536,12 +551,12 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
         Hk = K.shape[1]
         ks = _rows("K", K, ntok, Hk, d, dt)
         if K_out is None:
-            K_out = torch.empty((ntok, Hk, d), dtype=dt, device=Q.device)
+            K_out = _new_like(K)
         kos = _rows("K_out", K_out, ntok, Hk, d, dt)
         kargs = (Hk, K.data_ptr(), ks, K_out.data_ptr(), kos)
     else:
         _require(K_out is None, "K_out without K")
-    _call(Q.device, (Q, K, Q_out, K_out, start, cu_seqlens, rp.phases), load_library().mf_rope,
+    _call(Q.get_device(), (Q, K, Q_out, K_out, start, cu_seqlens, rp.phases), load_library().mf_rope,
           C.byref(rp._desc), C.byref(b), d, _dtype_code(dt), Hq, Q.data_ptr(), qs,
           Q_out.data_ptr(), qos, *kargs, int(bool(backward)))
     return Q_out if K is None else (Q_out, K_out)
@@ -553,12 +568,12 @@ class KVCache:
     is what mapped_av reads."""
 
     def __init__(self, K, V, page_table):
-        _require(K.dim() == 4 and K.shape == V.shape and K.dtype == V.dtype
-                 and K.is_contiguous() and V.is_contiguous(),
-                 "K and V must be contiguous pools [npages, page_size, Hkv, d] of one dtype")
-        _require(page_table.dtype == torch.int32 and page_table.dim() == 2
-                 and page_table.is_contiguous(),
-                 "page_table must be a contiguous int32 tensor [nseq, max_pages_per_seq]")
+        if (K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or not K.is_contiguous()
+                or not V.is_contiguous()):
+            _refuse("K and V must be contiguous pools [npages, page_size, Hkv, d] of one dtype")
+        if (page_table.dtype != torch.int32 or page_table.dim() != 2
+                or not page_table.is_contiguous()):
+            _refuse("page_table must be a contiguous int32 tensor [nseq, max_pages_per_seq]")
         self.K, self.V, self.page_table = K, V, page_table
         self.npages, self.page_size, self.Hkv, self.d = K.shape
         self.nseq, self.max_pages = page_table.shape
@@ -592,11 +607,11 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
         Hq = Q.shape[1]
         qs = _rows("Q", Q, ntok, Hq, d, dt)
         if Q_out is None:
-            Q_out = torch.empty((ntok, Hq, d), dtype=dt, device=Q.device)
+            Q_out = _new_like(Q)
         qargs = (Hq, Q.data_ptr(), qs, Q_out.data_ptr(), _rows("Q_out", Q_out, ntok, Hq, d, dt))
     else:
         _require(Q_out is None, "Q_out without Q")
-    _call(cache.K.device, (cache.V, cache.page_table, K, V, lens, Q, Q_out, cu_seqlens,
+    _call(cache.K.get_device(), (cache.V, cache.page_table, K, V, lens, Q, Q_out, cu_seqlens,
                            None if rope is None else rope.phases),
           load_library().mf_kv_append, C.byref(cache._desc),
           None if rope is None else C.byref(rope._desc), C.byref(b), K.data_ptr(), ks,
@@ -619,14 +634,13 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
     Hq = Q.shape[1]
     qs = _rows("Q", Q, nseq, Hq, d, dt)
     _index("lens", lens, nseq)
-    dev = Q.device
     if O is None:
-        O = torch.empty((nseq, Hq, d), dtype=dt, device=dev)
+        O = _new_like(Q)
     os_ = _rows("O", O, nseq, Hq, d, dt)
     if lse is None:
-        lse = torch.empty((Hq, nseq), dtype=torch.float32, device=dev)
-    _require(lse.dtype == torch.float32 and tuple(lse.shape) == (Hq, nseq)
-             and lse.is_contiguous(), "lse must be a contiguous float32 tensor [Hq, nseq]")
+        lse = Q.new_empty((Hq, nseq), dtype=torch.float32)
+    elif lse.dtype != torch.float32 or lse.shape != (Hq, nseq) or not lse.is_contiguous():
+        _refuse("lse must be a contiguous float32 tensor [Hq, nseq]")
     a = PagedAttnDesc(Hq, d ** -0.5 if scale is None else scale, band_bias, band_width, window,
                       len_add)
     cr, ar = C.byref(cache._desc), C.byref(a)
@@ -638,8 +652,8 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
                  "workspace must be a contiguous uint8 tensor")
         wsp = workspace.data_ptr() + (-workspace.data_ptr()) % 256
     else:
-        workspace, wsp = _workspace(nbytes, dev)
-    _call(dev, (cache.K, cache.V, cache.page_table, Q, O, lens, lse, workspace),
+        workspace, wsp = _workspace(nbytes, Q.device)
+    _call(Q.get_device(), (cache.K, cache.V, cache.page_table, Q, O, lens, lse, workspace),
           L.mf_paged_attn, cr, ar, lens.data_ptr(), Q.data_ptr(), qs, O.data_ptr(), os_,
           lse.data_ptr(), wsp, nbytes)
     return O, lse
