@@ -12,9 +12,14 @@
 // go to float32 half turns and sincospif.
 //
 // Bound by memory: every element is read and written once, a few FMAs each.
-// One thread keeps the sines of its VEC pairs in registers and walks the
-// token's heads (Q, K and V alike), so the sines are computed once per thread
-// and not read from a table, and all loads and stores are 16 bytes.
+// A block first places its tokens (sequence, position, page) and computes
+// their sines into shared memory, each once; then its warps walk the tokens'
+// heads (Q, K and V alike), two 16-byte packs a lane and step, and read the
+// sines where they are used.  Loads are hidden by the number of warps: six
+// blocks on an SM at 40 registers.  Measured at 32,768 tokens of 40 + 40 heads
+// of 128: sines kept in registers and four heads loaded ahead (115 registers,
+// two blocks) 317 us; two steps loaded ahead 257; as here 205 (6.6 TB/s).
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -25,6 +30,8 @@ namespace mf {
 namespace {
 
 constexpr int kRotaryThreads = 256;
+constexpr int kRotaryBlocks = 6;  // resident on an SM
+constexpr int kSms = 148;
 
 struct RotaryParams {
   // rotation (half = 0: none)
@@ -48,124 +55,163 @@ struct RotaryParams {
   int page_size, max_pages;
   int64_t npages;
   unsigned* status;
-  int units, slots;  // threads per head; heads in flight per token
+  int tokens;  // of a block
 };
+
+constexpr int kMaxTokens = 4;  // of a block
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
   T v[N];
 };
 
-// Two packs of VEC elements of one head: the pairs' first and second halves
-// (half layout), 2 VEC neighbours (interleaved), or 2 VEC copied elements.
-template <typename T, int VEC>
-struct Two {
-  Pack<T, VEC> a, b;
-};
-
+// A unit: two packs of VEC elements of one head: the first and second halves
+// of VEC pairs (half layout), 2 VEC neighbours (interleaved), or 2 VEC copied
+// elements.
 template <typename T, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotaryThreads) k_rotary(const RotaryParams p) {
-  constexpr int kBatch = 4;  // heads loaded before the first is stored
-  const int per_token = p.units * p.slots;
-  const int tokens = kRotaryThreads / per_token;
-  const int64_t t = int64_t(blockIdx.x) * tokens + threadIdx.x / per_token;
-  if (t >= p.ntok || threadIdx.x >= tokens * per_token) return;
-  const int u = threadIdx.x % p.units;
-  const int slot = threadIdx.x % per_token / p.units;
-
-  const int s = p.cu ? upper_index(p.cu, p.nseq, t) : int(t);
-  const int32_t first = p.start ? p.start[s] : 0;
-  const int64_t pos = int64_t(first) + (p.cu ? t - p.cu[s] : 0);
-  int64_t row = t;  // of K's and V's outputs
-  if (p.paged) {
-    if (first < 0) return;  // a padding sequence
-    int32_t at = -1;
-    if (pos >= 0 && pos < int64_t(p.max_pages) * p.page_size)
-      at = p.page_table[int64_t(s) * p.max_pages + int(pos) / p.page_size];
-    if (at < 0 || at >= p.npages) {
-      if (slot == 0 && u == 0) atomicOr(p.status, kStatusBadPage);
-      return;
-    }
-    row = int64_t(at) * p.page_size + int(pos) % p.page_size;
-  }
-
-  // units 0 .. half/VEC-1 rotate, the rest copy the dims past rot_dim
-  const bool rotates = u * VEC < p.half;
-  const int off_a = rotates && !INTERLEAVED ? u * VEC : 2 * u * VEC;
-  const int off_b = rotates && !INTERLEAVED ? p.half + u * VEC : 2 * u * VEC + VEC;
-  float co[VEC], si[VEC];
-  if (rotates) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      const uint64_t turns = uint64_t(pos) * p.phases[u * VEC + i];
-      const float half_turns = float(int32_t(turns >> 32)) * 0x1p-31f;
-      sincospif(half_turns, &si[i], &co[i]);
-      co[i] *= p.scale;
-      si[i] *= p.backward ? -p.scale : p.scale;
-    }
-  }
-
-  const T* q = static_cast<const T*>(p.Q) + t * p.q_stride;
-  const T* k = static_cast<const T*>(p.K) + t * p.k_stride;
-  const T* v = static_cast<const T*>(p.V) + t * p.v_stride;
-  T* qo = static_cast<T*>(p.Qo) + t * p.qo_stride;
-  T* ko = static_cast<T*>(p.Ko) + row * p.ko_stride;
-  T* vo = static_cast<T*>(p.Vo) + row * p.ko_stride;
-  const int H = p.Hq + p.Hk + p.Hv;
-  for (int h0 = slot; h0 < H; h0 += kBatch * p.slots) {
-    Two<T, VEC> x[kBatch];
-#pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      const int h = h0 + n * p.slots;
-      if (h >= H) break;
-      const T* in = h < p.Hq          ? q + int64_t(h) * p.d
-                    : h < p.Hq + p.Hk ? k + int64_t(h - p.Hq) * p.d
-                                      : v + int64_t(h - p.Hq - p.Hk) * p.d;
-      const bool turn = rotates && h < p.Hq + p.Hk;
-      // V's heads are copied at the same offsets, whatever the pairs are
-      x[n].a = *reinterpret_cast<const Pack<T, VEC>*>(in + off_a);
-      x[n].b = *reinterpret_cast<const Pack<T, VEC>*>(in + off_b);
-      if (turn) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          T& ra = !INTERLEAVED ? x[n].a.v[i] : 2 * i < VEC ? x[n].a.v[2 * i % VEC] : x[n].b.v[2 * i % VEC];
-          T& rb = !INTERLEAVED      ? x[n].b.v[i]
-                  : 2 * i + 1 < VEC ? x[n].a.v[(2 * i + 1) % VEC]
-                                    : x[n].b.v[(2 * i + 1) % VEC];
-          const float a = to_f32(ra), b = to_f32(rb);
-          ra = from_f32<T>(fmaf(a, co[i], -b * si[i]));
-          rb = from_f32<T>(fmaf(a, si[i], b * co[i]));
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      const int h = h0 + n * p.slots;
-      if (h >= H) break;
-      T* out = h < p.Hq          ? qo + int64_t(h) * p.d
-               : h < p.Hq + p.Hk ? ko + int64_t(h - p.Hq) * p.d
-                                 : vo + int64_t(h - p.Hq - p.Hk) * p.d;
-      *reinterpret_cast<Pack<T, VEC>*>(out + off_a) = x[n].a;
-      *reinterpret_cast<Pack<T, VEC>*>(out + off_b) = x[n].b;
-    }
+__device__ __forceinline__ void turn_pair(Pack<T, VEC>& a, Pack<T, VEC>& b, int i, float co,
+                                          float si) {
+  constexpr bool I = INTERLEAVED;
+  const bool first = 2 * i < VEC;
+  const T ta = !I ? a.v[i] : first ? a.v[2 * i % VEC] : b.v[2 * i % VEC];
+  const T tb = !I ? b.v[i] : 2 * i + 1 < VEC ? a.v[(2 * i + 1) % VEC] : b.v[(2 * i + 1) % VEC];
+  const float x = to_f32(ta), y = to_f32(tb);
+  const T ra = from_f32<T>(fmaf(x, co, -y * si)), rb = from_f32<T>(fmaf(x, si, y * co));
+  if (!I) {
+    a.v[i] = ra;
+    b.v[i] = rb;
+  } else {
+    if (first)
+      a.v[2 * i % VEC] = ra;
+    else
+      b.v[2 * i % VEC] = ra;
+    if (2 * i + 1 < VEC)
+      a.v[(2 * i + 1) % VEC] = rb;
+    else
+      b.v[(2 * i + 1) % VEC] = rb;
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool INTERLEAVED, int D>
+__global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks) k_rotary(const RotaryParams p) {
+  constexpr int kUnits = D / (2 * VEC);  // of a head
+  constexpr int kPairs = D / 2;
+  // cosines and sines, two pairs in a row: pairs 2 c and 2 c + 1 of unit u at
+  // [token][c][u], so that neighbouring lanes read neighbouring 16 bytes
+  constexpr int kC = VEC >= 2 ? VEC / 2 : 1, kIn = VEC >= 2 ? 2 : 1;
+  __shared__ alignas(16) float2 turns[kMaxTokens][kPairs];
+  __shared__ int64_t rows[kMaxTokens], positions[kMaxTokens];
+  const int64_t t0 = int64_t(blockIdx.x) * p.tokens;
+  const int live = int(min(int64_t(p.tokens), p.ntok - t0));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (threadIdx.x < live) {
+    const int64_t t = t0 + threadIdx.x;
+    const int s = p.cu ? upper_index(p.cu, p.nseq, t) : int(t);
+    const int32_t first = p.start ? p.start[s] : 0;
+    const int64_t pos = int64_t(first) + (p.cu ? t - p.cu[s] : 0);
+    int64_t row = t;  // of K's and V's outputs; -1: nothing is written
+    if (p.paged) {
+      row = -1;
+      if (first >= 0) {  // else a padding sequence
+        int32_t at = -1;
+        if (pos >= 0 && pos < int64_t(p.max_pages) * p.page_size)
+          at = p.page_table[int64_t(s) * p.max_pages + int(pos) / p.page_size];
+        if (at < 0 || at >= p.npages)
+          atomicOr(p.status, kStatusBadPage);
+        else
+          row = int64_t(at) * p.page_size + int(pos) % p.page_size;
+      }
+    }
+    rows[threadIdx.x] = row;
+    positions[threadIdx.x] = pos;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < live * kPairs; i += kRotaryThreads) {
+    const int token = i / kPairs, pair = i % kPairs;
+    if (pair >= p.half) continue;
+    const uint64_t angle = uint64_t(positions[token]) * p.phases[pair];
+    float si, co;
+    sincospif(float(int32_t(angle >> 32)) * 0x1p-31f, &si, &co);
+    const int u = pair / VEC, c = pair % VEC / kIn;
+    turns[token][(c * kUnits + u) * kIn + pair % kIn] =
+        make_float2(co * p.scale, si * (p.backward ? -p.scale : p.scale));
+  }
+  __syncthreads();
+
+  // 32 units a step; the warps take steps in turn
+  const int H = p.Hq + p.Hk + p.Hv, per_token = (H * kUnits + 31) / 32;
+  int token = 0;
+  for (int step = threadIdx.x / 32;; step += kRotaryThreads / 32) {
+    while (step >= per_token) {
+      step -= per_token;
+      ++token;
+    }
+    if (token >= live) break;
+    const int item = step * 32 + threadIdx.x % 32, h = item / kUnits, u = item % kUnits;
+    const int64_t t = t0 + token, row = rows[token];
+    if (h >= H || row < 0) continue;
+    const T* in;
+    T* out;
+    if (h < p.Hq) {
+      in = static_cast<const T*>(p.Q) + t * p.q_stride + h * D;
+      out = static_cast<T*>(p.Qo) + t * p.qo_stride + h * D;
+    } else if (h < p.Hq + p.Hk) {
+      in = static_cast<const T*>(p.K) + t * p.k_stride + (h - p.Hq) * D;
+      out = static_cast<T*>(p.Ko) + row * p.ko_stride + (h - p.Hq) * D;
+    } else {
+      in = static_cast<const T*>(p.V) + t * p.v_stride + (h - p.Hq - p.Hk) * D;
+      out = static_cast<T*>(p.Vo) + row * p.ko_stride + (h - p.Hq - p.Hk) * D;
+    }
+    // units 0 .. half/VEC-1 rotate, the rest copy the dims past rot_dim; V's
+    // are copied at the same offsets
+    const bool pairs = u * VEC < p.half;
+    const int off_a = pairs && !INTERLEAVED ? u * VEC : 2 * u * VEC;
+    const int off_b = off_a + (pairs && !INTERLEAVED ? p.half : VEC);
+    Pack<T, VEC> a = *reinterpret_cast<const Pack<T, VEC>*>(in + off_a);
+    Pack<T, VEC> b = *reinterpret_cast<const Pack<T, VEC>*>(in + off_b);
+    if (pairs && h < p.Hq + p.Hk) {
+      const float2* cs = &turns[token][u * kIn];
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        if constexpr (VEC >= 2) {
+          const float4 w = *reinterpret_cast<const float4*>(cs + c * kUnits * 2);
+          turn_pair<T, VEC, INTERLEAVED>(a, b, 2 * c, w.x, w.y);
+          turn_pair<T, VEC, INTERLEAVED>(a, b, 2 * c + 1, w.z, w.w);
+        } else {
+          turn_pair<T, VEC, INTERLEAVED>(a, b, 0, cs->x, cs->y);
+        }
+      }
+    }
+    *reinterpret_cast<Pack<T, VEC>*>(out + off_a) = a;
+    *reinterpret_cast<Pack<T, VEC>*>(out + off_b) = b;
+  }
+}
+
+template <typename T, int VEC, int D>
 cudaError_t launch_vec(RotaryParams& p, bool interleaved, cudaStream_t st) {
-  p.units = p.d / (2 * VEC);
-  // Heads in flight per token: all of a block's threads on one token when
-  // there are few tokens (latency), a quarter when they fill the GPU anyway,
-  // so that a thread's sines serve four times as many heads.
-  p.slots = kRotaryThreads / p.units;
-  if (p.ntok > 4 * 148) p.slots = p.slots >= 4 ? p.slots / 4 : 1;
-  const int tokens = kRotaryThreads / (p.units * p.slots);
-  const int64_t grid = (p.ntok + tokens - 1) / tokens;
-  if (interleaved)
-    k_rotary<T, VEC, true><<<unsigned(grid), kRotaryThreads, 0, st>>>(p);
-  else
-    k_rotary<T, VEC, false><<<unsigned(grid), kRotaryThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  // Tokens of a block: as many as leave every SM its blocks kTurns times
+  // over, so that the last ones to end hold up little, but where the tokens go
+  // round, enough of them for kSteps steps, against the block's fixed cost, and
+  // never more than kMaxTokens (32K tokens of 80 heads: 205 us with at most 4,
+  // 210 with 8, 217 without the limit; a packed float32 batch of 8 heads: 7.1
+  // us with 4 tokens each, 8.1 with 2).
+  constexpr int64_t kTurns = 4, kSteps = 20;
+  const int64_t steps = (int64_t(p.Hq + p.Hk + p.Hv) * (D / (2 * VEC)) + 31) / 32;
+  const int64_t many = p.ntok / (kSms * kRotaryBlocks * kTurns);
+  const int64_t enough = std::min((kSteps + steps - 1) / steps, p.ntok / kSms);
+  p.tokens = int(std::clamp<int64_t>(std::max(many, enough), 1, kMaxTokens));
+  cudaLaunchAttribute attr;  // it may take its place before the launch ahead has ended
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((p.ntok + p.tokens - 1) / p.tokens));
+  cfg.blockDim = dim3(kRotaryThreads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return interleaved ? cudaLaunchKernelEx(&cfg, k_rotary<T, VEC, true, D>, p)
+                     : cudaLaunchKernelEx(&cfg, k_rotary<T, VEC, false, D>, p);
 }
 
 // 16-byte packs need every row and both halves of the rotation on 16-byte
@@ -180,8 +226,11 @@ cudaError_t launch_rotary(RotaryParams& p, bool interleaved, cudaStream_t st) {
   const int64_t strides[] = {p.q_stride, p.qo_stride, p.k_stride, p.v_stride, p.ko_stride};
   for (int64_t x : strides) bits |= uintptr_t(x) * sizeof(T);
   bits |= uintptr_t(p.half) * sizeof(T);
-  return bits % 16 == 0 ? launch_vec<T, kVec>(p, interleaved, st)
-                        : launch_vec<T, 1>(p, interleaved, st);
+  if (p.d == 128)
+    return bits % 16 == 0 ? launch_vec<T, kVec, 128>(p, interleaved, st)
+                          : launch_vec<T, 1, 128>(p, interleaved, st);
+  return bits % 16 == 0 ? launch_vec<T, kVec, 64>(p, interleaved, st)
+                        : launch_vec<T, 1, 64>(p, interleaved, st);
 }
 
 mf_status fail(mf_status st, const char* msg) {
