@@ -4,7 +4,8 @@
 
 Objects go to cross_model_attention_block_b200/_build/, the library to
 cross_model_attention_block_b200/libmapflow.so.  A source is recompiled when it
-or any header is newer than its object.
+or any header is newer than its object.  The argument marshalling of the decode
+calls (csrc_py/, against torch's headers) becomes _marshal.so beside it.
 """
 from __future__ import annotations
 
@@ -21,6 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmapflow.so")
+MARSHAL_SRC = os.path.join(PKG, "csrc_py", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -51,6 +54,32 @@ def _compile(src, obj, verbose_ptxas=False):
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     return r.stderr
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile _marshal.so against the running interpreter's torch."""
+    hdr = os.path.join(ROOT, "include", "mapflow.h")
+    if not force and not _stale(MARSHAL_SRC, MARSHAL, os.path.getmtime(hdr)):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+           os.path.join(CUDA_HOME, "include"), os.path.join(troot, "include"),
+           os.path.join(troot, "include", "torch", "csrc", "api", "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for i in inc:
+        cmd += ["-isystem" if troot in i else "-I", i]
+    tmp = MARSHAL + ".tmp"
+    cmd += [MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(troot, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    shutil.move(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, jobs: int = 8, verbose_ptxas: bool = False) -> str:
@@ -85,6 +114,7 @@ def build(force: bool = False, jobs: int = 8, verbose_ptxas: bool = False) -> st
         shutil.move(tmp, LIB)
     if verbose_ptxas:
         print("\n".join(logs))
+    build_marshal(force)
     return LIB
 
 

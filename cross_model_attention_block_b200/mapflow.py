@@ -90,11 +90,12 @@ class MapflowError(RuntimeError):
 
 
 _lib = None
+_fast = None  # the decode calls' marshalling in C++ (csrc_py/marshal.cpp)
 
 
 def load_library(path: str = LIB_PATH):
     """Load libmapflow.so and declare its signatures (no GPU needed)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -148,7 +149,14 @@ def load_library(path: str = LIB_PATH):
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
-    _lib = L
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError("_marshal.so is missing or does not fit this torch: build it with "
+                           "`python -m cross_model_attention_block_b200.build`") from e
+    _marshal.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in (
+        "mf_rope", "mf_kv_append", "mf_paged_attn", "mf_paged_attn_workspace")))
+    _lib, _fast = L, _marshal
     return L
 
 
@@ -443,8 +451,16 @@ def _require(ok, msg):
         _refuse(msg)
 
 
-# The checks below run in every call of a decode step: messages are put together
-# only where one is refused.
+# The decode calls go through _fast, which checks its arguments, makes the call and
+# returns None where one is not of the plain kind; the checks below then say what is
+# wrong, or the call is made from here (on another device than the current one).
+
+def _made(r):
+    """The result of a call that _fast made: its outputs, unless it is a status."""
+    if type(r) is int:
+        _check(r)
+    return r
+
 
 def _rows(name, t, ntok, H, d, dtype):
     """Checks a [ntok, H, d] tensor whose heads are d apart; elements between tokens."""
@@ -502,6 +518,7 @@ class Rope:
         self.phases, self.interleaved, self.scale = phases, bool(interleaved), float(scale)
         self._desc = RopeDesc(2 * phases.shape[0], int(self.interleaved), phases.data_ptr(),
                               self.scale)
+        self._addr = C.addressof(self._desc)
 
     @classmethod
     def from_freqs(cls, inv_freq, interleaved=False, scale=1.0, device="cuda"):
@@ -536,6 +553,11 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     start[s] + t - cu_seqlens[s]; without cu_seqlens, start [ntok] holds every token's
     own position.  backward=True takes gradients of the outputs to those of the inputs.
     Q_out may be Q, and K_out may be K."""
+    if _fast is None:
+        load_library()
+    r = _fast.rope(rp._addr, rp.phases, Q, K, start, cu_seqlens, Q_out, K_out, backward)
+    if r is not None:
+        return _made(r)
     _require(start is not None or cu_seqlens is not None, "start or cu_seqlens must be given")
     _require(Q.dim() == 3, "Q must be [ntok, Hq, d]")
     ntok, Hq, d = Q.shape
@@ -580,6 +602,9 @@ class KVCache:
         self._desc = KvCacheDesc(K.data_ptr(), V.data_ptr(), page_table.data_ptr(), self.npages,
                                  self.page_size, self.max_pages, self.nseq, self.Hkv, self.d,
                                  _dtype_code(K.dtype))
+        self._addr = C.addressof(self._desc)
+        dev = K.get_device()
+        self._device = dev if V.get_device() == dev == page_table.get_device() else -1
 
     @classmethod
     def make(cls, npages, page_size, Hkv, d, dtype, page_table):
@@ -596,6 +621,13 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     without Q).  cu_seqlens [nseq + 1]: the new tokens of every sequence; None: one each.
     A negative length marks a padding sequence, whose rows are left as they were.
     `lens` itself is not changed."""
+    if _fast is None:
+        load_library()
+    r = _fast.kv_append(cache._addr, cache._device, K, V, lens,
+                        None if rope is None else rope._addr,
+                        None if rope is None else rope.phases, Q, Q_out, cu_seqlens)
+    if r is not None:
+        return None if r is True else _made(r)
     _require(K.dim() == 3, "K must be [ntok, Hkv, d]")
     ntok, dt, d = K.shape[0], cache.K.dtype, cache.d
     b = _batch(ntok, lens, cu_seqlens)
@@ -628,8 +660,18 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
     scale: 1/sqrt(d) by default; band_bias within band_width tokens, as the sender's
     logits; window: keys more than window - 1 tokens back are masked (0: none).
     `workspace` may be a uint8 device tensor reused across calls (one per call in flight)."""
+    if scale is None:
+        scale = cache.d ** -0.5
+    if _fast is None:
+        load_library()
+    r = _fast.paged_attn(cache._addr, cache._device, Q, lens, O, lse, workspace, len_add, scale,
+                         band_bias, band_width, window)
+    if r is not None:
+        return _made(r)
     L = load_library()
     nseq, d, dt = cache.nseq, cache.d, cache.K.dtype
+    for name, x in (("len_add", len_add), ("band_width", band_width), ("window", window)):
+        _require(-2 ** 31 <= x < 2 ** 31, f"{name} must fit in 32 bits")
     _require(Q.dim() == 3, "Q must be [nseq, Hq, d]")
     Hq = Q.shape[1]
     qs = _rows("Q", Q, nseq, Hq, d, dt)
@@ -641,7 +683,7 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
         lse = Q.new_empty((Hq, nseq), dtype=torch.float32)
     elif lse.dtype != torch.float32 or lse.shape != (Hq, nseq) or not lse.is_contiguous():
         _refuse("lse must be a contiguous float32 tensor [Hq, nseq]")
-    a = PagedAttnDesc(Hq, d ** -0.5 if scale is None else scale, band_bias, band_width, window,
+    a = PagedAttnDesc(Hq, scale, band_bias, band_width, window,
                       len_add)
     cr, ar = C.byref(cache._desc), C.byref(a)
     nbytes = L.mf_paged_attn_workspace(cr, ar)
