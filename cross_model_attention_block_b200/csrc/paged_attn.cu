@@ -38,6 +38,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kUnit = 16;      // keys of one unit
+constexpr int kRowCost = 2;    // of a row besides its units, in units
 constexpr int kCtas = 148;     // one block per SM of a B200
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -89,16 +90,18 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
   return k;
 }
 
-// The line of units cut into kCtas << shift equal runs, 1 << shift per block.
+// The line is made of the rows' units, each row's behind kRowCost places that
+// stand for what a row costs besides its units (queries, sums, output), and cut
+// into kCtas << shift equal runs, 1 << shift per block.
 struct Cuts {
   int64_t total;
   int shift;
-  // first unit of run w
+  // first place of run w
   __device__ __forceinline__ int64_t at(int w) const {
     const uint64_t x = uint64_t(total) * uint32_t(w);
     return int64_t((x >> 32 ? x / kCtas : uint32_t(x) / uint32_t(kCtas)) >> shift);
   }
-  // the run that holds unit u
+  // the run that holds place u
   __device__ __forceinline__ int holder(int64_t u) const {
     const uint64_t x = uint64_t(u + 1) * uint32_t(kCtas << shift) - 1;
     return x >> 32 ? int(x / uint64_t(total)) : int(uint32_t(x) / uint32_t(total));
@@ -115,15 +118,18 @@ __device__ __forceinline__ Cuts cuts_of(const Params& p, int64_t total) {
   return Cuts{total, shift};
 }
 
-// A place in the line of units.
+// A place in the line: a unit, and how much of the run is left from there.
 struct Walk {
   int s, r, g;  // sequence, its row, unit of the row
+  int left;     // <= 0: the run is over
   Span k;
   // the next unit; rows of a sequence have equally many
   __device__ __forceinline__ void step(const Params& p) {
+    --left;
     if (++g < k.n) return;
     g = 0;
-    if (++r < p.Hkv * p.groups) return;
+    left -= kRowCost;
+    if (left <= 0 || ++r < p.Hkv * p.groups) return;
     r = 0;
     do {
       if (++s >= p.nseq) return;
@@ -134,18 +140,19 @@ struct Walk {
 
 template <int THREADS>
 struct PlanSmem {
-  int64_t before[THREADS + 1];  // units of the sequences before thread t's
+  int64_t before[THREADS + 1];  // places of the sequences before thread t's
   int64_t warp_sum[THREADS / 32];
 };
 
-// Units of every thread's share of the sequences, added up over the block.
+// Places of every thread's share of the sequences, added up over the block.
 template <int THREADS>
 __device__ __forceinline__ void plan_units(const Params& p, PlanSmem<THREADS>& sm, bool report) {
   const int per = (p.nseq + THREADS - 1) / THREADS;
   const int s0 = min(int(threadIdx.x) * per, p.nseq), s1 = min(s0 + per, p.nseq);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
-    mine += span_of(p, s).n;
+    const int n = span_of(p, s).n;
+    mine += n > 0 ? n + kRowCost : 0;
     if (report && int64_t(p.lens[s]) + p.len_add > int64_t(p.max_pages) * p.page_size)
       atomicOr(p.status, kStatusBadPage);
   }
@@ -165,10 +172,12 @@ __device__ __forceinline__ void plan_units(const Params& p, PlanSmem<THREADS>& s
   __syncthreads();
 }
 
-// The place of unit u < before[THREADS] (the same u in the whole warp).
+// Where a run of `n` places from place u on begins: `into` is u's place in its
+// row, below kRowCost if it lies before the row's first unit.  The same u in
+// the whole warp.
 template <int THREADS>
-__device__ __forceinline__ Walk find_unit(const Params& p, const PlanSmem<THREADS>& sm,
-                                          int64_t u) {
+__device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem<THREADS>& sm, int64_t u,
+                                           int n, int* into) {
   constexpr int kSub = THREADS / 32;
   const int lane = threadIdx.x % 32;
   const int t0 = (__popc(__ballot_sync(0xffffffffu, sm.before[lane * kSub] <= u)) - 1) * kSub;
@@ -179,13 +188,16 @@ __device__ __forceinline__ Walk find_unit(const Params& p, const PlanSmem<THREAD
   const int rows = p.Hkv * p.groups;
   while (true) {
     w.k = span_of(p, w.s);
-    const int64_t n = int64_t(w.k.n) * rows;
-    if (at < n || w.s + 1 >= p.nseq) break;
-    at -= n;
+    const int64_t places = w.k.n > 0 ? int64_t(w.k.n + kRowCost) * rows : 0;
+    if (at < places || w.s + 1 >= p.nseq) break;
+    at -= places;
     ++w.s;
   }
-  w.r = at >> 32 ? int(at / w.k.n) : int(uint32_t(at) / uint32_t(w.k.n));
-  w.g = int(at - int64_t(w.r) * w.k.n);
+  const uint32_t row = w.k.n + kRowCost;
+  w.r = at >> 32 ? int(at / row) : int(uint32_t(at) / row);
+  *into = int(at - int64_t(w.r) * row);
+  w.g = max(0, *into - kRowCost);
+  w.left = n - max(0, kRowCost - *into);
   return w;
 }
 
@@ -679,14 +691,19 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     u0 = cuts.at(w);
     u1 = cuts.at(w + 1);
   }
-  const int n_units = int(u1 - u0);
   Walk at = {};
-  if (n_units > 0) at = find_unit<kThreads>(p, plan, u0);
+  bool mine = false;   // this block's whole run lies in one row
+  bool begun = false;  // the row the run begins in, at a unit of it
+  if (u1 > u0) {
+    int into;
+    at = find_place<kThreads>(p, plan, u0, int(u1 - u0), &into);
+    const int64_t row = u0 - into + kRowCost;  // its first unit
+    begun = u0 >= row;
+    mine = row <= c0 && row + at.k.n >= c1;
+  }
   if (lane == 0 && warp >> cuts.shift == 0) p.starts[w] = Start{at.s, at.r, at.g, at.k.n};
   if (w == 0 && lane == 0) *p.total = cuts.total;
-  // does this block's whole run lie in one row?
-  const bool together =
-      __syncthreads_or(n_units > 0 && u0 - at.g <= c0 && u0 - at.g + at.k.n >= c1) != 0;
+  join_ml[warp][lane] = make_float2(-INFINITY, 0.f);
 
   char* ring = smem + warp * kStages * S::kStageBytes;
   Body body(lane, smem + S::kRing + warp * Body::kScratch);
@@ -732,25 +749,29 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
         tma_load_4d(dst + Body::kTile, &tv, bar, 0, slot, 0, head);
       }
     }
-    if (++issued < n_units) {
+    ++issued;
+    if (ahead.left > 1) {
       const int s = ahead.s, r = ahead.r;
       ahead.step(p);
       // another row begins; its units have the same pages if they are still at hand
       if (ahead.s != s || (ahead.r != r && batch > 0)) batch = -1;
+    } else {
+      ahead.left = 0;
     }
   };
+#pragma unroll 1  // `issue` is long, and this runs once
   for (int i = 0; i < kStages; ++i)
-    if (issued < n_units) issue(i);
+    if (ahead.left > 0) issue(i);
 
   int done = 0, stage = 0;
   uint32_t phase = 0;
-  while (done < n_units && ok) {
+  while (at.left > 0 && ok) {
     const int group = at.r % p.groups, kvh = at.r / p.groups;
     const int h0 = kvh * p.G + group * p.gh, heads = min(p.gh, p.G - group * p.gh);
-    const int run = min(n_units - done, at.k.n - at.g);
-    const bool whole = at.g == 0 && run == at.k.n;
+    const int n = min(at.left, at.k.n - at.g);
+    const bool whole = at.g == 0 && n == at.k.n;
     body.begin(static_cast<const T*>(p.Q) + at.s * p.q_stride + int64_t(h0) * D, heads);
-    for (int i = 0; i < run; ++i) {
+    for (int i = 0; i < n; ++i) {
       ok = mbar_wait(&bars[warp][stage], phase, p.status);
       if (__any_sync(0xffffffffu, !ok)) {
         ok = false;
@@ -761,7 +782,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
         body.step(p, src, src + Body::kTile, (at.k.first + at.g + i) * kUnit, at.k);
       __syncwarp();
       ++done;
-      if (issued < n_units) issue(stage);
+      if (ahead.left > 0) issue(stage);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -769,13 +790,18 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     }
     if (!ok) break;
     body.finish();
-    if (together) break;  // one row: joined below
-    if (whole)
+    if (whole && !mine) {
       body.put(heads, Finished<T, D>{p, at.s, h0});
-    else
-      body.put(heads, piece_at<D>(p, done == run ? 2 * w : 2 * w + 1));
-    at.g += run - 1;
-    if (done < n_units) at.step(p);
+    } else {
+      PieceAt<D> to = piece_at<D>(p, begun ? 2 * w : 2 * w + 1);
+      if (mine) to = PieceAt<D>{reinterpret_cast<float*>(ring), join_ml[warp]};
+      body.put(heads, to);
+    }
+    begun = false;
+    if (mine) break;
+    at.g += n - 1;
+    at.left -= n - 1;
+    at.step(p);
   }
   // a wait that gave up: the copies still in flight end before the block does
   if (!ok)
@@ -787,18 +813,12 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
       }
     }
 
-  if (together) {
-    // the warps' pieces of the row, through the (now idle) ring
-    float* mine = reinterpret_cast<float*>(ring);
-    const int heads = min(p.gh, p.G - at.r % p.groups * p.gh);
-    join_ml[warp][lane] = make_float2(-INFINITY, 0.f);
-    __syncwarp();
-    if (n_units > 0 && ok) body.put(heads, PieceAt<D>{mine, join_ml[warp]});
-    // every block whose run is not empty has a warp whose run is not empty; the
-    // row is that of the first such warp
+  if (__syncthreads_or(mine)) {
+    // the warps' pieces of the row are in the (now idle) ring; the row is that
+    // of the first warp whose run is not empty
     __shared__ int row_s, row_r;
     __shared__ bool row_whole;
-    if (n_units > 0 && u0 == c0 && lane == 0) {
+    if (mine && u0 == c0 && lane == 0) {
       row_s = at.s;
       row_r = at.r;
       row_whole = at.g == 0 && c1 - c0 == at.k.n;
