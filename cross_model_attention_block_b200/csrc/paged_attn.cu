@@ -910,7 +910,7 @@ __device__ __forceinline__ void join_runs(const Params& p, const Row& row, const
     if (slot >= 0) ml = __ldcg(&p.part_ml[int64_t(slot) * p.gh + head]);
     unsigned left = __ballot_sync(0xffffffffu, slot >= 0);
     while (left) {
-      constexpr int kBatch = 8;
+      constexpr int kBatch = 3;
       float o[kBatch][D / 32];
       unsigned now = left;
 #pragma unroll
@@ -952,7 +952,7 @@ __device__ __forceinline__ void put_row(const Params& p, const Row& row, int hea
 }
 
 template <typename T, int D, int WARPS>  // WARPS of the main kernel's blocks
-__global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(const Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params p) {
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float2 sm_ml[kJoinWarps];
   const int head = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
