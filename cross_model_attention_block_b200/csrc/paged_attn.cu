@@ -40,10 +40,14 @@ namespace {
 constexpr int kUnit = 16;      // keys of one unit
 constexpr int kRowCost = 2;    // of a row besides its units, in units
 constexpr int kCtas = 148;     // one block per SM of a B200
+// A row's reference m is not its running maximum: it moves when a logit lies
+// more than 2^kSlack above it, about once a row, and only then are the sums
+// rescaled.  Weights stay below 2^kSlack.
+constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct Start {  // where a warp's run begins
+struct Start {  // where a block's run begins
   int s, r;     // sequence and row of the sequence
   int g, n;     // units of that row before the run, and in all
 };
@@ -57,13 +61,12 @@ struct Params {
   int64_t q_stride, o_stride, npages;
   int nseq, Hq, Hkv, G, page_size, max_pages, len_add, band, window;
   int groups, gh;  // groups of query heads per KV head, heads of a group
-  int min_run;     // units of a run, if there are fewer than that for every warp
   float scale2, bias2;  // times log2 e
-  // workspace: pieces of cut rows (two per warp: the row its run begins in,
-  // the row it ends in), where the runs begin, the number of units
-  float* part_o;   // [2 warps][gh][D]
-  float2* part_ml; // [2 warps][gh]
-  Start* starts;   // [warps]
+  // workspace: pieces of the rows that blocks share (two per block: of the row
+  // its run begins in and of the row it ends in), where the blocks begin
+  float* part_o;   // [2 blocks][gh][D]
+  float2* part_ml; // [2 blocks][gh]
+  Start* starts;   // [blocks]
   int64_t* total;
   unsigned* status;
 };
@@ -108,13 +111,12 @@ struct Cuts {
   }
 };
 
-// Runs shorter than this cost more in pieces to join than they save: a piece
-// (gh rows of float32, written and read once) is gh / 4 of a unit's bytes in
-// bf16, half that in float32.
+// One run for each of a block's warps; fewer warps where there are too few
+// places for that.
 template <int WARPS>
-__device__ __forceinline__ Cuts cuts_of(const Params& p, int64_t total) {
+__device__ __forceinline__ Cuts cuts_of(int64_t total) {
   int shift = WARPS == 8 ? 3 : 2;
-  while (shift > 0 && total < (int64_t(kCtas) << shift) * p.min_run) --shift;
+  while (shift > 0 && total < (int64_t(kCtas) << shift)) --shift;
   return Cuts{total, shift};
 }
 
@@ -172,12 +174,11 @@ __device__ __forceinline__ void plan_units(const Params& p, PlanSmem<THREADS>& s
   __syncthreads();
 }
 
-// Where a run of `n` places from place u on begins: `into` is u's place in its
-// row, below kRowCost if it lies before the row's first unit.  The same u in
-// the whole warp.
+// The first unit of the run of `n` places from place u on (the same in the
+// whole warp).
 template <int THREADS>
 __device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem<THREADS>& sm, int64_t u,
-                                           int n, int* into) {
+                                           int n) {
   constexpr int kSub = THREADS / 32;
   const int lane = threadIdx.x % 32;
   const int t0 = (__popc(__ballot_sync(0xffffffffu, sm.before[lane * kSub] <= u)) - 1) * kSub;
@@ -195,9 +196,9 @@ __device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem<THREA
   }
   const uint32_t row = w.k.n + kRowCost;
   w.r = at >> 32 ? int(at / row) : int(uint32_t(at) / row);
-  *into = int(at - int64_t(w.r) * row);
-  w.g = max(0, *into - kRowCost);
-  w.left = n - max(0, kRowCost - *into);
+  const int into = int(at - int64_t(w.r) * row);  // below kRowCost: before the row's units
+  w.g = max(0, into - kRowCost);
+  w.left = n - max(0, kRowCost - into);
   return w;
 }
 
@@ -249,15 +250,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int D_, int ROWS>  // ROWS: 8, 16 or 32 query heads of a group at most
+template <int D_, int HEADS>  // HEADS: 4, 8 or 16 query heads of a group at most
 struct Bf16Body {
   using T = __nv_bfloat16;
-  static constexpr int D = D_, kWarps = 8;
+  static constexpr int D = D_, kWarps = 8, kHeads = HEADS;
   static constexpr int kTile = kUnit * D * 2;
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? (HEADS == 4 ? 3 : 2) : (HEADS == 16 ? 5 : 6);
   static constexpr int kScratch = 0;  // bytes of shared memory per warp besides the ring
-  static constexpr bool kPacked = ROWS == 8;
-  static constexpr int NB = ROWS == 32 ? 2 : 1;  // 16-row products
+  static constexpr bool kPacked = HEADS <= 8;
+  static constexpr int NB = 1;                   // 16-row products
   static constexpr int NR = kPacked ? 1 : 2;     // rows of one product a thread holds
   static constexpr int KS = D / 16;
 
@@ -344,7 +345,7 @@ struct Bf16Body {
         float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (__any_sync(0xffffffffu, mx > m[b][n])) {
+        if (__any_sync(0xffffffffu, mx > m[b][n] + kSlack)) {
           const Join f(m[b][n], mx);
           m[b][n] = f.m;
           l[b][n] *= f.ca;
@@ -439,9 +440,9 @@ struct Bf16Body {
 template <int D_, int GT>  // GT: query heads of a group at most (even)
 struct F32Body {
   using T = float;
-  static constexpr int D = D_, kWarps = D == 128 ? 4 : 8;
+  static constexpr int D = D_, kWarps = D == 128 ? 4 : 8, kHeads = GT;
   static constexpr int kTile = kUnit * D * 4;
-  static constexpr int kStages = GT == 16 ? 2 : 3;
+  static constexpr int kStages = GT == 4 ? 3 : 2;
   // queries [GT][D], weights [16 keys][GT][2], factors [GT]
   static constexpr int kScratch = GT * D * 4 + kUnit * GT * 8 + GT * 4 + 64;
   static constexpr int NO = D / 32;       // dims a lane owns
@@ -509,7 +510,7 @@ struct F32Body {
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1)
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
-      up |= mx[i] > m[i];
+      up |= mx[i] > m[i] + kSlack;
     }
     const bool any_up = __any_sync(0xffffffffu, up);
     if (any_up) {
@@ -644,13 +645,45 @@ __device__ __forceinline__ PieceAt<D> piece_at(const Params& p, int64_t slot) {
   return PieceAt<D>{p.part_o + slot * p.gh * D, p.part_ml + slot * p.gh};
 }
 
+template <int D>
+struct Piece {  // running joint result; a lane owns D / 32 dims
+  float m = -INFINITY, l = 0.f, o[D / 32] = {};
+  __device__ __forceinline__ void add(float m2, float l2, const float* o2) {
+    const Join f(m, m2);
+    m = f.m;
+    l = fmaf(l, f.ca, l2 * f.cb);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], f.ca, o2[i] * f.cb);
+  }
+};
+
+template <int D, class Sink>
+__device__ __forceinline__ void put_row(const Sink& sink, int head, const Piece<D>& x) {
+  const int lane = threadIdx.x % 32;
+  const auto to = sink.row(head, x.m, x.l, lane == 0);
+#pragma unroll
+  for (int i = 0; i < D / 32; i += 2) to.store(lane * (D / 32) + i, x.o[i], x.o[i + 1]);
+}
+
 // ------------------------------------------------------------ the main kernel
+
+// What a warp tells its block of its run: the rows it shares with its
+// neighbours (sequence, row of it; s < 0: none), and whether the first goes on
+// past the run.
+struct Cut {
+  int s, r, through;  // the row the run begins in, if the run before has a part
+  int s_end, r_end;   // the row it ends in, if only the runs after have another
+  int any;            // the run is not empty
+};
 
 template <class Body>
 struct Shared {
   static constexpr int kStageBytes = 2 * Body::kTile;
   static constexpr int kRing = Body::kWarps * Body::kStages * kStageBytes;
-  static constexpr int kBytes = kRing + Body::kWarps * Body::kScratch + 1024;  // 1024: alignment
+  static constexpr int kPiece = Body::kHeads * Body::D * 4;  // a row's sums
+  static constexpr int kOffPieces = kRing + Body::kWarps * Body::kScratch;
+  static constexpr int kBytes = kOffPieces + Body::kWarps * kPiece + 1024;  // 1024: alignment
+  static_assert(Body::kStages * kStageBytes >= kPiece);
 };
 
 template <class Body>
@@ -665,7 +698,10 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PlanSmem<kThreads> plan;
   __shared__ uint64_t bars[kWarps][kStages];
-  __shared__ float2 join_ml[kWarps][32];
+  // the pieces of rows that the block's warps share: [0] of the row a warp's run
+  // begins in, [1] of the row it ends in
+  __shared__ float2 join_ml[2][kWarps][Body::kHeads];
+  __shared__ Cut cuts_in[kWarps];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (lane == 0) {
@@ -683,7 +719,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   // the joining kernel may take its place now; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const Cuts cuts = cuts_of<kWarps>(p, plan.before[kThreads]);
+  const Cuts cuts = cuts_of<kWarps>(plan.before[kThreads]);
   const int w0 = blockIdx.x << cuts.shift, w = w0 + warp;
   const int64_t c0 = cuts.at(w0), c1 = cuts.at(w0 + (1 << cuts.shift));
   int64_t u0 = c1, u1 = c1;
@@ -692,18 +728,14 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     u1 = cuts.at(w + 1);
   }
   Walk at = {};
-  bool mine = false;   // this block's whole run lies in one row
-  bool begun = false;  // the row the run begins in, at a unit of it
+  bool begun = false;  // the row the run begins in is begun before it
   if (u1 > u0) {
-    int into;
-    at = find_place<kThreads>(p, plan, u0, int(u1 - u0), &into);
-    const int64_t row = u0 - into + kRowCost;  // its first unit
-    begun = u0 >= row;
-    mine = row <= c0 && row + at.k.n >= c1;
+    at = find_place<kThreads>(p, plan, u0, int(u1 - u0));
+    begun = at.g > 0;
+    if (lane == 0 && u0 == c0) p.starts[blockIdx.x] = Start{at.s, at.r, at.g, at.k.n};
   }
-  if (lane == 0 && warp >> cuts.shift == 0) p.starts[w] = Start{at.s, at.r, at.g, at.k.n};
-  if (w == 0 && lane == 0) *p.total = cuts.total;
-  join_ml[warp][lane] = make_float2(-INFINITY, 0.f);
+  if (threadIdx.x == 0 && blockIdx.x == 0) *p.total = cuts.total;
+  Cut cut{-1, 0, 0, -1, 0, at.left > 0};
 
   char* ring = smem + warp * kStages * S::kStageBytes;
   Body body(lane, smem + S::kRing + warp * Body::kScratch);
@@ -790,15 +822,20 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     }
     if (!ok) break;
     body.finish();
-    if (whole && !mine) {
+    if (whole) {
       body.put(heads, Finished<T, D>{p, at.s, h0});
     } else {
-      PieceAt<D> to = piece_at<D>(p, begun ? 2 * w : 2 * w + 1);
-      if (mine) to = PieceAt<D>{reinterpret_cast<float*>(ring), join_ml[warp]};
-      body.put(heads, to);
+      // the first row's piece keeps out of the ring, which may be in use; the
+      // last's, when all is read, goes there
+      const int end = begun ? 0 : 1;
+      float* to = reinterpret_cast<float*>(begun ? smem + S::kOffPieces + warp * S::kPiece : ring);
+      body.put(heads, PieceAt<D>{to, join_ml[end][warp]});
+      if (begun)
+        cut.s = at.s, cut.r = at.r, cut.through = at.g + n < at.k.n;
+      else
+        cut.s_end = at.s, cut.r_end = at.r;
     }
     begun = false;
-    if (mine) break;
     at.g += n - 1;
     at.left -= n - 1;
     at.step(p);
@@ -813,43 +850,57 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
       }
     }
 
-  if (__syncthreads_or(mine)) {
-    // the warps' pieces of the row are in the (now idle) ring; the row is that
-    // of the first warp whose run is not empty
-    __shared__ int row_s, row_r;
-    __shared__ bool row_whole;
-    if (mine && u0 == c0 && lane == 0) {
-      row_s = at.s;
-      row_r = at.r;
-      row_whole = at.g == 0 && c1 - c0 == at.k.n;
-    }
-    __syncthreads();
-    const int g2 = row_r % p.groups, hh = row_r / p.groups * p.G + g2 * p.gh;
-    const int nh = min(p.gh, p.G - g2 * p.gh);
-    for (int i = threadIdx.x; i < nh * (D / 2); i += kThreads) {
-      const int h = i / (D / 2), d = i % (D / 2) * 2;
-      float2 ml[kWarps], t[kWarps];
-      float m = -INFINITY, l = 0.f, a = 0.f, b = 0.f;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        ml[v] = join_ml[v][h];
-        t[v] = *reinterpret_cast<const float2*>(smem + v * kStages * S::kStageBytes +
-                                                (h * D + d) * 4);
-        m = fmaxf(m, ml[v].x);
+  // ---- the rows that the block's warps share.  A chain of pieces begins with a
+  // warp's last row, or with the row the block begins in, and goes on over the
+  // next warps' first rows.
+  if (lane == 0) cuts_in[warp] = cut;
+  __syncthreads();
+  {
+    const Cut c = cuts_in[lane % kWarps];
+    const bool one = lane < kWarps;
+    const uint32_t any = __ballot_sync(0xffffffffu, one && c.any);
+    const uint32_t first = __ballot_sync(0xffffffffu, one && c.s >= 0);
+    const uint32_t through = __ballot_sync(0xffffffffu, one && c.s >= 0 && c.through);
+    const uint32_t last = __ballot_sync(0xffffffffu, one && c.s_end >= 0);
+    // chain v: of warp v's last row; chain -1: of the block's first
+    int turn = 0;
+    for (int v = -1; v < kWarps; ++v) {
+      const int lead = v < 0 ? __ffs(any) - 1 : v;  // the warp of its first piece
+      if (lead < 0 || !(((v < 0 ? first : last) >> lead) & 1)) continue;
+      const Cut& of = cuts_in[lead];
+      const int s = v < 0 ? of.s : of.s_end, r = v < 0 ? of.r : of.r_end;
+      const int group = r % p.groups, heads = min(p.gh, p.G - group * p.gh);
+      bool open = v >= 0 || ((through >> lead) & 1);  // goes on after the pieces so far
+      uint32_t more = 0;                              // warps with its further pieces
+      for (uint32_t w = any >> 1 >> lead << 1 << lead; w && open; w &= w - 1) {
+        more |= w & -w;
+        open = through & w & -w;
       }
-      const float ref = m == -INFINITY ? 0.f : m;
+      // the warps take the chains' heads in turn
+      const int mine = (warp - turn) & (kWarps - 1);
+      turn += heads;
+      for (int h = mine; h < heads; h += kWarps) {
+        Piece<D> acc;
+        auto add = [&](const char* from, float2 ml) {
+          if (ml.y == 0.f) return;  // nothing seen: its sums are void
+          float o[D / 32];
+          const float* x = reinterpret_cast<const float*>(from) + h * D + lane * (D / 32);
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        const float c = ex2(ml[v].x - ref);
-        const bool some = ml[v].y != 0.f;  // else its sums are not there
-        l = fmaf(ml[v].y, c, l);
-        a = fmaf(some ? t[v].x : 0.f, c, a);
-        b = fmaf(some ? t[v].y : 0.f, c, b);
+          for (int i = 0; i < D / 32; ++i) o[i] = x[i];
+          acc.add(ml.x, ml.y, o);
+        };
+        add(v < 0 ? smem + S::kOffPieces + lead * S::kPiece
+                  : smem + lead * kStages * S::kStageBytes,
+            join_ml[v < 0 ? 0 : 1][lead][h]);
+        for (uint32_t w = more; w; w &= w - 1) {
+          const int k = __ffs(w) - 1;
+          add(smem + S::kOffPieces + k * S::kPiece, join_ml[0][k][h]);
+        }
+        if (v >= 0 && !open)
+          put_row(Finished<T, D>{p, s, r / p.groups * p.G + group * p.gh}, h, acc);
+        else
+          put_row(piece_at<D>(p, 2 * blockIdx.x + (v < 0 ? 0 : 1)), h, acc);
       }
-      if (row_whole)
-        Finished<T, D>{p, row_s, hh}.row(h, m, l, d == 0).store(d, a, b);
-      else
-        piece_at<D>(p, int64_t(2) * w0).row(h, m, l, d == 0).store(d, a, b);
     }
   }
   // sequences without keys
@@ -864,48 +915,25 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
 
 // ---------------------------------------------------------- joining the rows
 
-// One warp per cut that is the first inside its row, and a query head
-// (blockIdx.y); a row of many pieces takes the whole block.
+// One warp per block boundary that is the first inside its row, and a query
+// head (blockIdx.y); a row that many blocks share takes the whole block.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinAlone = 8;  // runs of a row that one warp joins by itself
-
-template <int D>
-struct Piece {  // running joint result; a lane owns D / 32 dims
-  float m = -INFINITY, l = 0.f, o[D / 32] = {};
-  __device__ __forceinline__ void add(float m2, float l2, const float* o2) {
-    const Join f(m, m2);
-    m = f.m;
-    l = fmaf(l, f.ca, l2 * f.cb);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = fmaf(o[i], f.ca, o2[i] * f.cb);
-  }
-};
+constexpr int kJoinAlone = 8;  // blocks of a row whose pieces one warp joins by itself
 
 struct Row {
-  int64_t a, e;  // units
+  int64_t a, e;  // places of its units
   int s, r;
-  int v0, v1;    // first and last run that holds one of them
+  int v0, v1;    // first and last block that holds one of them
 };
 
 template <int D>
-__device__ __forceinline__ void join_runs(const Params& p, const Row& row, const Cuts& cuts,
-                                          int head, int warp, int warps, Piece<D>& acc) {
+__device__ __forceinline__ void join_blocks(const Params& p, const Row& row, const Cuts& cuts,
+                                            int head, int warp, int warps, Piece<D>& acc) {
   const int lane = threadIdx.x % 32;
-  // eights of runs go round the warps, so that the pieces of whole blocks do too
-  for (int base = row.v0 & ~7; base <= row.v1; base += 32 * warps) {
-    const int v = base + (lane / 8 * warps + warp) * 8 + lane % 8;
+  for (int base = row.v0; base <= row.v1; base += 32 * warps) {
+    const int v = base + lane * warps + warp;
     int slot = -1;
-    if (v >= row.v0 && v <= row.v1) {
-      const int64_t u0 = cuts.at(v), u1 = cuts.at(v + 1);
-      const int w0 = v >> cuts.shift << cuts.shift;
-      const int64_t c0 = cuts.at(w0), c1 = cuts.at(w0 + (1 << cuts.shift));
-      if (u0 < u1) {
-        if (c0 >= row.a && c1 <= row.e)  // joined by its block
-          slot = u0 == c0 ? 2 * w0 : -1;
-        else
-          slot = u0 >= row.a ? 2 * v : 2 * v + 1;
-      }
-    }
+    if (v <= row.v1 && cuts.at(v) < cuts.at(v + 1)) slot = 2 * v + (cuts.at(v) > row.a ? 0 : 1);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (slot >= 0) ml = __ldcg(&p.part_ml[int64_t(slot) * p.gh + head]);
     unsigned left = __ballot_sync(0xffffffffu, slot >= 0);
@@ -941,45 +969,29 @@ __device__ __forceinline__ void join_runs(const Params& p, const Row& row, const
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void put_row(const Params& p, const Row& row, int head,
-                                        const Piece<D>& x) {
-  const int group = row.r % p.groups;
-  const int lane = threadIdx.x % 32;
-  const Finished<T, D> sink{p, row.s, row.r / p.groups * p.G + group * p.gh};
-  const auto to = sink.row(head, x.m, x.l, lane == 0);
-#pragma unroll
-  for (int i = 0; i < D / 32; i += 2) to.store(lane * (D / 32) + i, x.o[i], x.o[i + 1]);
-}
-
-template <typename T, int D, int WARPS>  // WARPS of the main kernel's blocks
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params p) {
   __shared__ float sm_o[kJoinWarps][D];
   __shared__ float2 sm_ml[kJoinWarps];
   const int head = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int w = blockIdx.x * kJoinWarps + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Start st = lane < kJoinWarps ? p.starts[w] : Start{};
-  const Cuts cuts = cuts_of<WARPS>(p, *p.total);
-  if (blockIdx.x * kJoinWarps >= kCtas << cuts.shift) return;
+  const Start st = lane < kJoinWarps && w < kCtas ? p.starts[w] : Start{};
+  const Cuts cuts{*p.total, 0};
 
-  // lane i: the cut before run blockIdx.x * 8 + i
+  // lane i: the boundary before block blockIdx.x * 8 + i
   Row row = {};
   bool split = false;
-  if (lane < kJoinWarps && w > 0 && w < kCtas << cuts.shift) {
+  if (lane < kJoinWarps && w > 0 && w < kCtas) {
     const int64_t u = cuts.at(w);
-    const int group = st.r % p.groups, heads = min(p.gh, p.G - group * p.gh);
-    if (cuts.at(w + 1) > u && st.g > 0 && head < heads) {
+    if (cuts.at(w + 1) > u && st.g > 0 && head < min(p.gh, p.G - st.r % p.groups * p.gh)) {
       row = Row{u - st.g, u - st.g + st.n, st.s, st.r, 0, 0};
-      // the first cut inside the row: the run before, the last that is not
-      // empty, begins no later than the row
-      const bool full = cuts.total >= kCtas << cuts.shift;
+      // the first inside the row: the block before, the last that is not empty,
+      // begins no later than the row
+      const bool full = cuts.total >= kCtas;
       split = row.a >= (full ? cuts.at(w - 1) : u - 1);
       if (split) {
         row.v0 = full ? w - 1 : cuts.holder(row.a);
         row.v1 = cuts.holder(row.e - 1);
-        const int w0 = row.v0 >> cuts.shift << cuts.shift;
-        // a block that held just this row is done with it
-        if (row.a == cuts.at(w0) && row.e == cuts.at(w0 + (1 << cuts.shift))) split = false;
       }
     }
   }
@@ -995,17 +1007,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
     x.v1 = __shfl_sync(0xffffffffu, row.v1, i);
     return x;
   };
+  auto finish = [&](const Row& x, const Piece<D>& acc) {
+    put_row(Finished<T, D>{p, x.s, x.r / p.groups * p.G + x.r % p.groups * p.gh}, head, acc);
+  };
   if ((mine >> warp) & 1) {
     const Row x = row_of(warp);
     Piece<D> acc;
-    join_runs<D>(p, x, cuts, head, 0, 1, acc);
-    put_row<T, D>(p, x, head, acc);
+    join_blocks<D>(p, x, cuts, head, 0, 1, acc);
+    finish(x, acc);
   }
   while (shared) {  // the same in every warp
     const Row x = row_of(__ffs(shared) - 1);
     shared &= shared - 1;
     Piece<D> acc;
-    join_runs<D>(p, x, cuts, head, warp, kJoinWarps, acc);
+    join_blocks<D>(p, x, cuts, head, warp, kJoinWarps, acc);
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) sm_o[warp][lane * (D / 32) + d] = acc.o[d];
@@ -1019,7 +1034,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
         for (int d = 0; d < D / 32; ++d) o[d] = sm_o[v][lane * (D / 32) + d];
         all.add(sm_ml[v].x, sm_ml[v].y, o);
       }
-      put_row<T, D>(p, x, head, all);
+      finish(x, all);
     }
   }
 }
@@ -1046,27 +1061,19 @@ mf_status check(const mf_kv_cache* cache, const mf_paged_attn_desc* a) {
 }
 
 // Query heads of one KV head are taken together, up to what a warp's registers
-// hold (32 for bf16, 16 for float32); more are cut into even groups, each of
-// which reads the keys again.
-int head_groups(const mf_kv_cache& c, int Hq) {
-  const int G = Hq / c.Hkv, most = c.dt == MF_BF16 ? 32 : 16;
-  return (G + most - 1) / most;
-}
-
-int warps_of(const mf_kv_cache& c) { return c.dt == MF_F32 && c.d == 128 ? 4 : 8; }
+// hold (16); more are cut into even groups, each of which reads the keys again.
+int head_groups(const mf_kv_cache& c, int Hq) { return (Hq / c.Hkv + 15) / 16; }
 
 size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   const int groups = head_groups(c, Hq), G = Hq / c.Hkv, gh = (G + groups - 1) / groups;
-  const size_t runs = size_t(kCtas) * warps_of(c);
   Carve k(ws);
-  float* part_o = k.take<float>(2 * runs * gh * c.d);
-  float2* part_ml = k.take<float2>(2 * runs * gh);
-  Start* starts = k.take<Start>(runs);
+  float* part_o = k.take<float>(size_t(2 * kCtas) * gh * c.d);
+  float2* part_ml = k.take<float2>(size_t(2 * kCtas) * gh);
+  Start* starts = k.take<Start>(kCtas);
   int64_t* total = k.take<int64_t>(1);
   if (p) {
     p->groups = groups;
     p->gh = gh;
-    p->min_run = std::max(1, gh / (c.dt == MF_BF16 ? 8 : 16));
     p->part_o = part_o;
     p->part_ml = part_ml;
     p->starts = starts;
@@ -1104,19 +1111,19 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_paged_attn<Body>, tk, tv, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((kCtas * Body::kWarps + kJoinWarps - 1) / kJoinWarps, p.gh);
+  cfg.gridDim = dim3((kCtas + kJoinWarps - 1) / kJoinWarps, p.gh);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_paged_join<typename Body::T, Body::D, Body::kWarps>, p);
+  return cudaLaunchKernelEx(&cfg, k_paged_join<typename Body::T, Body::D>, p);
 }
 
 template <int D>
 cudaError_t launch_d(const Params& p, mf_dtype dt, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   if (dt == MF_BF16) {
+    if (p.gh <= 4) return launch<Bf16Body<D, 4>>(p, tk, tv, st);
     if (p.gh <= 8) return launch<Bf16Body<D, 8>>(p, tk, tv, st);
-    if (p.gh <= 16) return launch<Bf16Body<D, 16>>(p, tk, tv, st);
-    return launch<Bf16Body<D, 32>>(p, tk, tv, st);
+    return launch<Bf16Body<D, 16>>(p, tk, tv, st);
   }
   if (p.gh <= 4) return launch<F32Body<D, 4>>(p, tk, tv, st);
   if (p.gh <= 8) return launch<F32Body<D, 8>>(p, tk, tv, st);
