@@ -94,31 +94,23 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
 }
 
 // The line is made of the rows' units, each row's behind kRowCost places that
-// stand for what a row costs besides its units (queries, sums, output), and cut
-// into kCtas << shift equal runs, 1 << shift per block.
+// stand for what a row costs besides its units (queries, sums, output).  It is
+// cut into kCtas << SHIFT equal runs: one for each warp of a block (SHIFT 2 or
+// 3), or, the same cuts at the blocks, one for each block (SHIFT 0).
+template <int SHIFT>
 struct Cuts {
   int64_t total;
-  int shift;
   // first place of run w
   __device__ __forceinline__ int64_t at(int w) const {
     const uint64_t x = uint64_t(total) * uint32_t(w);
-    return int64_t((x >> 32 ? x / kCtas : uint32_t(x) / uint32_t(kCtas)) >> shift);
+    return int64_t((x >> 32 ? x / kCtas : uint32_t(x) / uint32_t(kCtas)) >> SHIFT);
   }
   // the run that holds place u
   __device__ __forceinline__ int holder(int64_t u) const {
-    const uint64_t x = uint64_t(u + 1) * uint32_t(kCtas << shift) - 1;
+    const uint64_t x = uint64_t(u + 1) * uint32_t(kCtas << SHIFT) - 1;
     return x >> 32 ? int(x / uint64_t(total)) : int(uint32_t(x) / uint32_t(total));
   }
 };
-
-// One run for each of a block's warps; fewer warps where there are too few
-// places for that.
-template <int WARPS>
-__device__ __forceinline__ Cuts cuts_of(int64_t total) {
-  int shift = WARPS == 8 ? 3 : 2;
-  while (shift > 0 && total < (int64_t(kCtas) << shift)) --shift;
-  return Cuts{total, shift};
-}
 
 // A place in the line: a unit, and how much of the run is left from there.
 struct Walk {
@@ -719,14 +711,9 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   // the joining kernel may take its place now; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const Cuts cuts = cuts_of<kWarps>(plan.before[kThreads]);
-  const int w0 = blockIdx.x << cuts.shift, w = w0 + warp;
-  const int64_t c0 = cuts.at(w0), c1 = cuts.at(w0 + (1 << cuts.shift));
-  int64_t u0 = c1, u1 = c1;
-  if (warp >> cuts.shift == 0) {
-    u0 = cuts.at(w);
-    u1 = cuts.at(w + 1);
-  }
+  const Cuts<kWarps == 8 ? 3 : 2> cuts{plan.before[kThreads]};
+  const int w0 = blockIdx.x * kWarps, w = w0 + warp;
+  const int64_t c0 = cuts.at(w0), u0 = cuts.at(w), u1 = cuts.at(w + 1);
   Walk at = {};
   bool begun = false;  // the row the run begins in is begun before it
   if (u1 > u0) {
@@ -927,7 +914,7 @@ struct Row {
 };
 
 template <int D>
-__device__ __forceinline__ void join_blocks(const Params& p, const Row& row, const Cuts& cuts,
+__device__ __forceinline__ void join_blocks(const Params& p, const Row& row, const Cuts<0>& cuts,
                                             int head, int warp, int warps, Piece<D>& acc) {
   const int lane = threadIdx.x % 32;
   for (int base = row.v0; base <= row.v1; base += 32 * warps) {
@@ -976,7 +963,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
   const int w = blockIdx.x * kJoinWarps + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Start st = lane < kJoinWarps && w < kCtas ? p.starts[w] : Start{};
-  const Cuts cuts{*p.total, 0};
+  const Cuts<0> cuts{*p.total};
 
   // lane i: the boundary before block blockIdx.x * 8 + i
   Row row = {};
