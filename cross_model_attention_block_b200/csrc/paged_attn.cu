@@ -61,6 +61,7 @@ struct Params {
   int64_t q_stride, o_stride, npages;
   int nseq, Hq, Hkv, G, page_size, max_pages, len_add, band, window;
   int groups, gh;  // groups of query heads per KV head, heads of a group
+  bool by_rows;    // blocks take whole rows
   float scale2, bias2;  // times log2 e
   // workspace: pieces of the rows that blocks share (two per block: of the row
   // its run begins in and of the row it ends in), where the blocks begin
@@ -164,6 +165,23 @@ __device__ __forceinline__ void plan_units(const Params& p, PlanSmem<THREADS>& s
   sm.before[threadIdx.x] = sum - mine;
   if (threadIdx.x == THREADS - 1) sm.before[THREADS] = sum;
   __syncthreads();
+}
+
+// The place where the row before which `row` others come begins; rows of
+// sequences without keys count, but have no places.
+template <int THREADS>
+__device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem<THREADS>& sm,
+                                                int64_t row) {
+  const int rows = p.Hkv * p.groups, s = int(row / rows);
+  if (s >= p.nseq) return sm.before[THREADS];
+  const int per = (p.nseq + THREADS - 1) / THREADS, t = s / per;
+  int64_t at = sm.before[t];
+  for (int i = t * per; i < s; ++i) {
+    const int n = span_of(p, i).n;
+    at += n > 0 ? int64_t(n + kRowCost) * rows : 0;
+  }
+  const int n = span_of(p, s).n;
+  return at + (n > 0 ? (row - int64_t(s) * rows) * (n + kRowCost) : 0);
 }
 
 // The first unit of the run of `n` places from place u on (the same in the
@@ -713,7 +731,14 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
 
   const Cuts<kWarps == 8 ? 3 : 2> cuts{plan.before[kThreads]};
   const int w0 = blockIdx.x * kWarps, w = w0 + warp;
-  const int64_t c0 = cuts.at(w0), u0 = cuts.at(w), u1 = cuts.at(w + 1);
+  int64_t c0 = cuts.at(w0), u0 = cuts.at(w), u1 = cuts.at(w + 1);
+  if (p.by_rows) {
+    const int64_t rows = int64_t(p.nseq) * p.Hkv * p.groups;
+    c0 = place_of_row<kThreads>(p, plan, rows * blockIdx.x / kCtas);
+    const int64_t n = place_of_row<kThreads>(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0;
+    u0 = c0 + n * warp / kWarps;
+    u1 = c0 + n * (warp + 1) / kWarps;
+  }
   Walk at = {};
   bool begun = false;  // the row the run begins in is begun before it
   if (u1 > u0) {
@@ -1051,6 +1076,21 @@ mf_status check(const mf_kv_cache* cache, const mf_paged_attn_desc* a) {
 // hold (16); more are cut into even groups, each of which reads the keys again.
 int head_groups(const mf_kv_cache& c, int Hq) { return (Hq / c.Hkv + 15) / 16; }
 
+int warps_of(const mf_kv_cache& c) { return c.dt == MF_F32 && c.d == 128 ? 4 : 8; }
+
+// Where the table has room for few places a block, blocks take whole rows:
+// nothing is left to join, and the second launch, 1 to 3 of the 7 to 10 us
+// that short rows take, is not made.  Few: those that its warps are through
+// with in that time (14 sequences of up to 215 tokens, 8 heads a KV head: 11.1
+// us with the second launch, 9.0 without; float32 with 10 heads a KV head and
+// 29 units a row: 15.5 with, 32 without).
+bool whole_rows(const mf_kv_cache& c, int gh, int groups) {
+  const int64_t few = warps_of(c) * (c.dt == MF_BF16 ? 4 : gh <= 4 ? 7 : 2);
+  const int64_t places = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) + kRowCost;
+  const int64_t rows = int64_t(c.nseq) * c.Hkv * groups;
+  return places <= few && (rows + kCtas - 1) / kCtas * places <= few;
+}
+
 size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   const int groups = head_groups(c, Hq), G = Hq / c.Hkv, gh = (G + groups - 1) / groups;
   Carve k(ws);
@@ -1061,6 +1101,7 @@ size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   if (p) {
     p->groups = groups;
     p->gh = gh;
+    p->by_rows = whole_rows(c, gh, groups);
     p->part_o = part_o;
     p->part_ml = part_ml;
     p->starts = starts;
@@ -1097,7 +1138,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_paged_attn<Body>, tk, tv, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.by_rows) return e;
   cfg.gridDim = dim3((kCtas + kJoinWarps - 1) / kJoinWarps, p.gh);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
