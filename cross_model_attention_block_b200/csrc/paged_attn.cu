@@ -47,9 +47,9 @@ constexpr float kSlack = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct Start {  // where a block's run begins
-  int s, r;     // sequence and row of the sequence
-  int g, n;     // units of that row before the run, and in all
+struct Shared {  // a row that blocks v0 .. v1 share (v1 < v0: none)
+  int s, r;      // sequence and row of the sequence
+  int v0, v1;
 };
 
 struct Params {
@@ -64,11 +64,11 @@ struct Params {
   bool by_rows;    // blocks take whole rows
   float scale2, bias2;  // times log2 e
   // workspace: pieces of the rows that blocks share (two per block: of the row
-  // its run begins in and of the row it ends in), where the blocks begin
+  // its run begins in and of the row it ends in); entry b of `shared`: the row
+  // whose first block boundary is the one before block b
   float* part_o;   // [2 blocks][gh][D]
   float2* part_ml; // [2 blocks][gh]
-  Start* starts;   // [blocks]
-  int64_t* total;
+  Shared* shared;  // [blocks]
   unsigned* status;
 };
 
@@ -687,7 +687,7 @@ struct Cut {
 };
 
 template <class Body>
-struct Shared {
+struct Layout {
   static constexpr int kStageBytes = 2 * Body::kTile;
   static constexpr int kRing = Body::kWarps * Body::kStages * kStageBytes;
   static constexpr int kPiece = Body::kHeads * Body::D * 4;  // a row's sums
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     k_paged_attn(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const Params p) {
   using T = typename Body::T;
-  using S = Shared<Body>;
+  using S = Layout<Body>;
   constexpr int D = Body::D, kWarps = Body::kWarps, kStages = Body::kStages;
   constexpr int kThreads = kWarps * 32;
   extern __shared__ char smem_raw[];
@@ -744,9 +744,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   if (u1 > u0) {
     at = find_place<kThreads>(p, plan, u0, int(u1 - u0));
     begun = at.g > 0;
-    if (lane == 0 && u0 == c0) p.starts[blockIdx.x] = Start{at.s, at.r, at.g, at.k.n};
   }
-  if (threadIdx.x == 0 && blockIdx.x == 0) *p.total = cuts.total;
   Cut cut{-1, 0, 0, -1, 0, at.left > 0};
 
   char* ring = smem + warp * kStages * S::kStageBytes;
@@ -806,6 +804,25 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
 #pragma unroll 1  // `issue` is long, and this runs once
   for (int i = 0; i < kStages; ++i)
     if (ahead.left > 0) issue(i);
+
+  // ---- while they are on their way: the row to join that the block begins in
+  if (!p.by_rows && lane == 0) {
+    if (u0 == c0 && u1 > u0) {
+      const Cuts<0> blocks{cuts.total};
+      const int64_t row = u0 - at.g;  // its first unit, if that is before the block
+      const bool full = cuts.total >= kCtas;  // else blocks hold a place or none
+      Shared x{at.s, at.r, 0, -1};
+      if (begun && row >= (full ? blocks.at(blockIdx.x - 1) : u0 - 1)) {
+        x.v0 = full ? blockIdx.x - 1 : blocks.holder(row);
+        x.v1 = blocks.holder(row + at.k.n - 1);
+      }
+      p.shared[blockIdx.x] = x;
+    } else if (warp == 0 && cuts.at(w0 + kWarps) == c0) {  // an empty block
+      p.shared[blockIdx.x] = Shared{0, 0, 0, -1};
+      for (int i = 0; i < 2 * p.gh; ++i)
+        p.part_ml[int64_t(2) * blockIdx.x * p.gh + i] = make_float2(-INFINITY, 0.f);
+    }
+  }
 
   int done = 0, stage = 0;
   uint32_t phase = 0;
@@ -874,11 +891,14 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
     const uint32_t first = __ballot_sync(0xffffffffu, one && c.s >= 0);
     const uint32_t through = __ballot_sync(0xffffffffu, one && c.s >= 0 && c.through);
     const uint32_t last = __ballot_sync(0xffffffffu, one && c.s_end >= 0);
-    // chain v: of warp v's last row; chain -1: of the block's first
-    int turn = 0;
-    for (int v = -1; v < kWarps; ++v) {
+    // chain 0: of the block's first row, chain v + 1: of warp v's last
+    const uint32_t chains = (first & any & -any ? 1u : 0u) | last << 1;
+    const int share = min(p.gh, kWarps);  // warps that take a chain's heads in turn
+    for (int t = warp; t < __popc(chains) * share; t += kWarps) {
+      uint32_t rest = chains;
+      for (int i = t / share; i > 0; --i) rest &= rest - 1;
+      const int v = __ffs(rest) - 2;
       const int lead = v < 0 ? __ffs(any) - 1 : v;  // the warp of its first piece
-      if (lead < 0 || !(((v < 0 ? first : last) >> lead) & 1)) continue;
       const Cut& of = cuts_in[lead];
       const int s = v < 0 ? of.s : of.s_end, r = v < 0 ? of.r : of.r_end;
       const int group = r % p.groups, heads = min(p.gh, p.G - group * p.gh);
@@ -888,10 +908,7 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
         more |= w & -w;
         open = through & w & -w;
       }
-      // the warps take the chains' heads in turn
-      const int mine = (warp - turn) & (kWarps - 1);
-      turn += heads;
-      for (int h = mine; h < heads; h += kWarps) {
+      for (int h = t % share; h < heads; h += share) {
         Piece<D> acc;
         auto add = [&](const char* from, float2 ml) {
           if (ml.y == 0.f) return;  // nothing seen: its sums are void
@@ -932,20 +949,13 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAlone = 8;  // blocks of a row whose pieces one warp joins by itself
 
-struct Row {
-  int64_t a, e;  // places of its units
-  int s, r;
-  int v0, v1;    // first and last block that holds one of them
-};
-
 template <int D>
-__device__ __forceinline__ void join_blocks(const Params& p, const Row& row, const Cuts<0>& cuts,
-                                            int head, int warp, int warps, Piece<D>& acc) {
+__device__ __forceinline__ void join_blocks(const Params& p, const Shared& row, int head, int warp,
+                                            int warps, Piece<D>& acc) {
   const int lane = threadIdx.x % 32;
   for (int base = row.v0; base <= row.v1; base += 32 * warps) {
     const int v = base + lane * warps + warp;
-    int slot = -1;
-    if (v <= row.v1 && cuts.at(v) < cuts.at(v + 1)) slot = 2 * v + (cuts.at(v) > row.a ? 0 : 1);
+    const int slot = v <= row.v1 ? 2 * v + (v == row.v0) : -1;
     float2 ml = make_float2(-INFINITY, 0.f);
     if (slot >= 0) ml = __ldcg(&p.part_ml[int64_t(slot) * p.gh + head]);
     unsigned left = __ballot_sync(0xffffffffu, slot >= 0);
@@ -987,52 +997,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
   const int head = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int w = blockIdx.x * kJoinWarps + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Start st = lane < kJoinWarps && w < kCtas ? p.starts[w] : Start{};
-  const Cuts<0> cuts{*p.total};
-
   // lane i: the boundary before block blockIdx.x * 8 + i
-  Row row = {};
-  bool split = false;
-  if (lane < kJoinWarps && w > 0 && w < kCtas) {
-    const int64_t u = cuts.at(w);
-    if (cuts.at(w + 1) > u && st.g > 0 && head < min(p.gh, p.G - st.r % p.groups * p.gh)) {
-      row = Row{u - st.g, u - st.g + st.n, st.s, st.r, 0, 0};
-      // the first inside the row: the block before, the last that is not empty,
-      // begins no later than the row
-      const bool full = cuts.total >= kCtas;
-      split = row.a >= (full ? cuts.at(w - 1) : u - 1);
-      if (split) {
-        row.v0 = full ? w - 1 : cuts.holder(row.a);
-        row.v1 = cuts.holder(row.e - 1);
-      }
-    }
-  }
+  Shared row{0, 0, 0, -1};
+  if (lane < kJoinWarps && w < kCtas) row = p.shared[w];
+  const bool split = row.v0 <= row.v1 && head < min(p.gh, p.G - row.r % p.groups * p.gh);
   const unsigned mine = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 < kJoinAlone);
   unsigned shared = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 >= kJoinAlone);
   auto row_of = [&](int i) {
-    Row x;
-    x.a = __shfl_sync(0xffffffffu, row.a, i);
-    x.e = __shfl_sync(0xffffffffu, row.e, i);
-    x.s = __shfl_sync(0xffffffffu, row.s, i);
-    x.r = __shfl_sync(0xffffffffu, row.r, i);
-    x.v0 = __shfl_sync(0xffffffffu, row.v0, i);
-    x.v1 = __shfl_sync(0xffffffffu, row.v1, i);
-    return x;
+    return Shared{__shfl_sync(0xffffffffu, row.s, i), __shfl_sync(0xffffffffu, row.r, i),
+                  __shfl_sync(0xffffffffu, row.v0, i), __shfl_sync(0xffffffffu, row.v1, i)};
   };
-  auto finish = [&](const Row& x, const Piece<D>& acc) {
+  auto finish = [&](const Shared& x, const Piece<D>& acc) {
     put_row(Finished<T, D>{p, x.s, x.r / p.groups * p.G + x.r % p.groups * p.gh}, head, acc);
   };
   if ((mine >> warp) & 1) {
-    const Row x = row_of(warp);
+    const Shared x = row_of(warp);
     Piece<D> acc;
-    join_blocks<D>(p, x, cuts, head, 0, 1, acc);
+    join_blocks<D>(p, x, head, 0, 1, acc);
     finish(x, acc);
   }
   while (shared) {  // the same in every warp
-    const Row x = row_of(__ffs(shared) - 1);
+    const Shared x = row_of(__ffs(shared) - 1);
     shared &= shared - 1;
     Piece<D> acc;
-    join_blocks<D>(p, x, cuts, head, warp, kJoinWarps, acc);
+    join_blocks<D>(p, x, head, warp, kJoinWarps, acc);
     __syncthreads();
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) sm_o[warp][lane * (D / 32) + d] = acc.o[d];
@@ -1096,16 +1084,14 @@ size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   Carve k(ws);
   float* part_o = k.take<float>(size_t(2 * kCtas) * gh * c.d);
   float2* part_ml = k.take<float2>(size_t(2 * kCtas) * gh);
-  Start* starts = k.take<Start>(kCtas);
-  int64_t* total = k.take<int64_t>(1);
+  Shared* shared = k.take<Shared>(kCtas);
   if (p) {
     p->groups = groups;
     p->gh = gh;
     p->by_rows = whole_rows(c, gh, groups);
     p->part_o = part_o;
     p->part_ml = part_ml;
-    p->starts = starts;
-    p->total = total;
+    p->shared = shared;
   }
   return (k.used + 255) & ~size_t(255);
 }
@@ -1113,7 +1099,7 @@ size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
 template <class Body>
 cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv,
                    cudaStream_t st) {
-  constexpr int kSmem = Shared<Body>::kBytes;
+  constexpr int kSmem = Layout<Body>::kBytes;
   // once per device: the call costs as much as a fifth of a launch
   static std::atomic<uint64_t> set{0};
   int dev = 0;
