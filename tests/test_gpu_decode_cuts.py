@@ -1,0 +1,312 @@
+"""The single-token attention's division of work, its marshalling, and the rotation's launch
+shapes on the GPU, where they can go wrong: rows cut between warps and blocks at every kind of
+place, short tables, many sequences, logits that climb, captured calls whose lengths change.
+
+The plain 64-bit evaluations and the tolerances derived beside them are those of
+test_gpu_decode.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from cross_model_attention_block_b200 import mapflow as mfb
+from tests.test_gpu_decode import (BF, F32, attend64, check_attention, filled_cache, i32,
+                                   near_rotated, pages, randn, slots)
+
+pytestmark = pytest.mark.gpu
+
+
+def widened(c, width):
+    """The same cache behind a table with room for `width` pages a sequence."""
+    t = torch.full((c.nseq, width), -1, dtype=torch.int32, device="cuda")
+    t[:, :c.max_pages] = c.page_table
+    return mfb.KVCache(c.K, c.V, t)
+
+
+def mixed(seed, n, hi):
+    """Lengths: most short, some long, some empty."""
+    r = np.random.default_rng(seed)
+    x = np.exp(r.uniform(0, math.log(hi), n)).astype(int)
+    x[r.random(n) < 0.1] = 0
+    return x.tolist()
+
+
+# ------------------------------------------------------------------ cuts
+
+# head groups of every kernel variant: 1..4, 5..8 and 9..16 heads a group, and groups of groups
+LAYOUTS = [(BF, 8, 8, 128), (BF, 12, 4, 64), (BF, 14, 2, 128), (BF, 16, 2, 64), (BF, 22, 2, 128),
+           (BF, 16, 1, 64), (BF, 17, 1, 128), (BF, 64, 2, 64), (F32, 6, 6, 64), (F32, 8, 2, 128),
+           (F32, 7, 1, 64), (F32, 16, 2, 128), (F32, 13, 1, 64), (F32, 33, 1, 128)]
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,d", LAYOUTS)
+@pytest.mark.parametrize("lengths", [mixed(1, 40, 3000), mixed(2, 300, 40), [9000, 1, 0, 16, 4097]],
+                         ids=["spread", "many_short", "few_long"])
+def test_rows_cut_anywhere(dt, Hq, Hkv, d, lengths):
+    """Whole rows, rows over several warps, over several blocks; behind a table just wide enough
+    and behind a wide one (another division of the work)."""
+    c = filled_cache(lengths, 16, Hkv, d, dt, 50)
+    Q = randn((len(lengths), Hq, d), dt, 51)
+    for k in (c, widened(c, c.max_pages + 700)):
+        O, lse = mfb.paged_attn(k, Q, i32(lengths))
+        mfb.sync_status()
+        check_attention(c, lengths, Q, O, lse, d ** -0.5)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("total", [1, 2, 31, 147, 148, 149, 295, 297, 1183, 1185])
+def test_totals_around_the_numbers_of_blocks_and_warps(dt, total):
+    """One long row, and two, of about as many 16-key units as there are blocks or warps."""
+    for lengths in ([16 * total], [16 * total - 5, 16 * (total // 2) + 3]):
+        c = filled_cache(lengths, 16, 1, 64, dt, 52)
+        c = widened(c, c.max_pages + 40)
+        Q = randn((len(lengths), 3, 64), dt, 53)
+        O, lse = mfb.paged_attn(c, Q, i32(lengths))
+        mfb.sync_status()
+        check_attention(c, lengths, Q, O, lse, 64 ** -0.5)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_many_sequences(dt):
+    """More sequences than a block has threads, empty ones among them, windows inside."""
+    r = np.random.default_rng(3)
+    lengths = r.integers(0, 60, 1500).tolist()
+    for window in (0, 21):
+        c = filled_cache(lengths, 16, 2, 64, dt, 54, window=window)
+        Q = randn((len(lengths), 4, 64), dt, 55)
+        O, lse = mfb.paged_attn(c, Q, i32(lengths), window=window, band_bias=1.5, band_width=9)
+        mfb.sync_status()
+        some = list(range(0, 1500, 37)) + [1499]
+        for s in some:
+            L = lengths[s]
+            if L == 0:
+                assert (O[s] == 0).all() and (lse[:, s] == -math.inf).all()
+                continue
+            at = slots(c.page_table, 16, s, 0, L)
+            for h in range(2):
+                K = c.K.view(-1, 2, 64)[at, h].double()
+                V = c.V.view(-1, 2, 64)[at, h].double()
+                if window:
+                    K[:max(0, L - window)], V[:max(0, L - window)] = 0.0, 0.0
+                o, e, tol, delta = attend64(Q[s, 2 * h:2 * h + 2].double(), K, V, 0.125, 1.5, 9,
+                                            window)
+                got = O[s, 2 * h:2 * h + 2].double()
+                assert ((got - o).abs() <= tol + torch.finfo(dt).eps / 2 * o.abs()).all()
+                err = (lse[2 * h:2 * h + 2, s].double() - e).abs()
+                assert (err <= delta + 2.0 ** -22 * e.abs()).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("order", ["climbing", "falling", "steps"])
+def test_logits_that_climb_and_fall(dt, order):
+    """Logits that rise by more than the reference's slack again and again, fall, or jump: the
+    sums are rescaled in the middle of a row, and pieces of very different size meet."""
+    L, d, Hkv, G = 2500, 64, 2, 5
+    c = filled_cache([L, 40], 16, Hkv, d, dt, 56)
+    at = slots(c.page_table, 16, 0, 0, L)
+    ramp = torch.linspace(0.0, 60.0, L, device="cuda")
+    size = {"climbing": ramp, "falling": ramp.flip(0), "steps": torch.floor(ramp / 15) * 15}[order]
+    Q = randn((2, Hkv * G, d), dt, 57).abs() + 0.1
+    Q[:, :, 1:] *= 0.1
+    c.K.view(-1, Hkv, d)[at, :, 0] = size[:, None].to(dt)
+    O, lse = mfb.paged_attn(c, Q, i32([L, 40]), scale=1.0)
+    mfb.sync_status()
+    check_attention(c, [L, 40], Q, O, lse, 1.0)
+
+
+def test_a_group_of_256_heads():
+    lengths = [70, 0, 333]
+    c = filled_cache(lengths, 16, 1, 128, BF, 58)
+    Q = randn((3, 256, 128), BF, 59)
+    O, lse = mfb.paged_attn(c, Q, i32(lengths))
+    mfb.sync_status()
+    check_attention(c, lengths, Q, O, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_bad_pages_in_long_rows(dt):
+    """Every third page of a row outside the pool: its other keys alone take part."""
+    L, ps = 3000, 48
+    c = filled_cache([L, 50], ps, 1, 64, dt, 60)
+    good = c.page_table.clone()
+    c.page_table[0, ::3] = c.npages + 5
+    Q = randn((2, 4, 64), dt, 61)
+    O, lse = mfb.paged_attn(c, Q, i32([L, 50]))
+    with pytest.raises(mfb.MapflowError):
+        mfb.sync_status()
+    j = torch.arange(L, device="cuda")
+    kept = slots(good, ps, 0, 0, L)[(j // ps) % 3 != 0]
+    o, e, tol, delta = attend64(Q[0].double(), c.K.view(-1, 64)[kept].double(),
+                                c.V.view(-1, 64)[kept].double(), 0.125, 0.0, 0, 0)
+    assert ((O[0].double() - o).abs() <= tol + torch.finfo(dt).eps / 2 * o.abs()).all()
+    assert ((lse[:, 0].double() - e).abs() <= delta + 2.0 ** -22 * e.abs()).all()
+    c.page_table.fill_(-1)                                   # nothing left
+    O, lse = mfb.paged_attn(c, Q, i32([L, 50]))
+    with pytest.raises(mfb.MapflowError):
+        mfb.sync_status()
+    assert (O == 0).all() and (lse == -math.inf).all()
+
+
+# ------------------------------------------------------------------ captured calls
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_captured_call_follows_its_lengths(dt):
+    """One captured call, replayed with other lengths and queries: from empty to the whole
+    table, the cuts at other places each time; the bits of a call made outside a graph."""
+    full = [4000, 17, 900, 2500]
+    c = filled_cache(full, 16, 2, 64, dt, 62)
+    Q, lens = randn((4, 8, 64), dt, 63), i32([0, 0, 0, 0])
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    O, lse = mfb.paged_attn(c, Q, lens, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mfb.paged_attn(c, Q, lens, O=O, lse=lse, workspace=ws)
+    for k, now in enumerate(([0, 0, 0, 0], [1, 17, 0, 33], full, [4000, 0, 0, 0], [15, 16, 17, 2500])):
+        lens.copy_(i32(now))
+        Q.copy_(randn((4, 8, 64), dt, 64 + k))
+        O.fill_(7.0)
+        graph.replay()
+        got, got_lse = O.clone(), lse.clone()
+        want = mfb.paged_attn(c, Q, lens)
+        assert torch.equal(got, want[0]) and torch.equal(got_lse, want[1])
+        check_attention(c, now, Q, got, got_lse, 0.125)
+    mfb.sync_status()
+
+
+def test_append_and_attention_overlap_their_launches():
+    """A chain of small calls, each of which may be launched before the one ahead has ended,
+    with a torch kernel between them now and then: the results of the same calls with a
+    synchronization after each."""
+    def run(wait):
+        table, n = pages([540, 44, 108], 16, 70)
+        kv = mfb.KVCache(randn((n, 16, 2, 128), BF, 70), randn((n, 16, 2, 128), BF, 76), table)
+        lens, rp = i32([496, 0, 64]), mfb.Rope.make(128)
+        x = randn((3, 8 + 4, 128), BF, 71)
+        outs = []
+        for k in range(40):
+            q = mfb.kv_append(kv, x[:, 8:10], x[:, 10:], lens, rope=rp, Q=x[:, :8])
+            if wait:
+                torch.cuda.synchronize()
+            O, lse = mfb.paged_attn(kv, q, lens, len_add=1)
+            if wait:
+                torch.cuda.synchronize()
+            if k % 3 == 0:
+                x = x.roll(1, 0)
+            x[:, :8] = O
+            lens.add_(1)
+            outs += [O, lse]
+        mfb.sync_status()
+        return outs
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ marshalling
+
+def test_outputs_given_are_the_outputs_returned():
+    lengths = [100, 37]
+    c = filled_cache(lengths, 16, 2, 64, F32, 72)
+    Q, L = randn((2, 4, 64), F32, 73), i32(lengths)
+    O, lse = mfb.paged_attn(c, Q, L)
+    O2, lse2, ws = torch.empty_like(O), torch.empty_like(lse), torch.empty(64, dtype=torch.uint8,
+                                                                          device="cuda")
+    a, b = mfb.paged_attn(c, Q, L, O=O2, lse=lse2, workspace=ws)   # too small: one is made
+    assert a is O2 and b is lse2 and torch.equal(a, O) and torch.equal(b, lse)
+    assert mfb.paged_attn(c, Q, L, scale=1)[0].shape == O.shape    # a whole number as scale
+    rp = mfb.Rope.make(64)
+    q = mfb.rope(rp, Q, start=L)
+    q2, k2 = torch.empty_like(Q), torch.empty_like(Q)
+    a, b = mfb.rope(rp, Q, Q, start=L, Q_out=q2, K_out=k2)
+    assert a is q2 and b is k2 and torch.equal(q2, q) and torch.equal(k2, q)
+    assert mfb.kv_append(c, Q[:, :2], Q[:, 2:], i32([0, 0])) is None
+    q3 = torch.empty_like(Q)
+    assert mfb.kv_append(c, Q[:, :2], Q[:, 2:], i32([0, 0]), rope=rp, Q=Q, Q_out=q3) is q3
+    assert torch.equal(q3, mfb.rope(rp, Q, start=i32([0, 0])))
+
+
+def refused(f, *a, **kw):
+    with pytest.raises((mfb.MapflowError, ValueError)) as e:
+        f(*a, **kw)
+    assert str(e.value)
+
+
+def test_refusals_with_tensors_on_the_gpu():
+    c = filled_cache([40, 40], 16, 2, 64, F32, 74)
+    Q, L = randn((2, 4, 64), F32, 75), i32([40, 40])
+    refused(mfb.paged_attn, c, Q, L.long())
+    refused(mfb.paged_attn, c, Q, L.cpu())
+    refused(mfb.paged_attn, c, Q.bfloat16(), L)
+    refused(mfb.paged_attn, c, Q[:, :3], L)
+    refused(mfb.paged_attn, c, Q.transpose(1, 2), L)
+    refused(mfb.paged_attn, c, Q, L, window=-1)
+    refused(mfb.paged_attn, c, Q, L, window=1 << 40)
+    refused(mfb.paged_attn, c, Q, L, len_add=-(1 << 40))
+    refused(mfb.paged_attn, c, Q, L, scale=float("nan"))
+    refused(mfb.paged_attn, c, Q, L, lse=torch.empty(2, 4, device="cuda"))
+    refused(mfb.paged_attn, c, Q, L, O=torch.empty(2, 4, 64))
+    refused(mfb.paged_attn, c, Q, L, workspace=torch.empty(8 << 20, dtype=torch.int8,
+                                                           device="cuda"))
+    refused(mfb.paged_attn, c, torch.empty(2, 514, 64, device="cuda"), L)
+    rp = mfb.Rope.make(64)
+    refused(mfb.rope, rp, Q)
+    refused(mfb.rope, rp, Q, start=L[:1])
+    refused(mfb.rope, rp, Q, start=L.cpu())
+    refused(mfb.rope, rp, Q, Q.bfloat16(), start=L)
+    refused(mfb.rope, rp, Q, start=L, K_out=Q)
+    refused(mfb.rope, mfb.Rope.make(128), Q, start=L)
+    refused(mfb.kv_append, c, Q, Q, L)
+    refused(mfb.kv_append, c, Q[:, :2], Q[:, :2].bfloat16(), L)
+    refused(mfb.kv_append, c, Q[:, :2], Q[:, 2:], L[:1])
+    refused(mfb.kv_append, c, Q[:, :2], Q[:, 2:], L, rope=mfb.Rope.make(128))
+    refused(mfb.kv_append, c, Q[:, :2], Q[:, 2:], i32([0]), cu_seqlens=i32([0, 2]))
+    mfb.sync_status()                                        # nothing was launched
+
+
+# ------------------------------------------------------------------ rotation
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("ntok,Hq,Hk,d,rot", [(1, 1, 0, 64, 64), (3, 1, 1, 64, 32),
+                                              (5, 3, 2, 128, 128), (148, 2, 1, 64, 64),
+                                              (297, 1, 1, 64, 48), (3551, 4, 4, 64, 64),
+                                              (3552, 4, 4, 64, 64), (20000, 1, 1, 64, 16),
+                                              (40001, 2, 2, 128, 128), (2, 300, 1, 128, 20)])
+def test_rope_launch_shapes(dt, ntok, Hq, Hk, d, rot):
+    """Tokens that share a block or have one each, heads that fill half a step or many; the
+    last block with fewer tokens."""
+    f = mfb.rope_freqs(rot)
+    seqs = [ntok // 3, 0, ntok - ntok // 3]
+    start = [11, 5, 70000]
+    pos = torch.cat([torch.arange(s, s + m) for s, m in zip(start, seqs)])
+    Q = randn((ntok, Hq, d), dt, 80)
+    K = randn((ntok, Hk, d), dt, 81) if Hk else None
+    for inter in (False, True):
+        out = mfb.rope(mfb.Rope.from_freqs(f, inter), Q, K, start=i32(start),
+                       cu_seqlens=i32(np.concatenate([[0], np.cumsum(seqs)])))
+        for x, y in zip((Q, K), out if Hk else (out,)):
+            near_rotated(y, x, pos, f, rot, inter)
+
+
+def test_append_padding_sequences_between_prompts():
+    """Packed prompts with padding sequences among them: their tokens' rows stay as they were."""
+    new, past = [20, 7, 33, 5], [3, -1, 0, -4]
+    table, npages = pages([23, 7, 33, 5], 16, 82)
+    c = mfb.KVCache(randn((npages, 16, 2, 64), BF, 83), randn((npages, 16, 2, 64), BF, 84), table)
+    K0 = c.K.clone()
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    x = randn((sum(new), 4 + 2 + 2, 64), BF, 85)
+    f = mfb.rope_freqs(64)
+    Qo = torch.full((sum(new), 4, 64), 9.0, dtype=BF, device="cuda")
+    mfb.kv_append(c, x[:, 4:6], x[:, 6:], i32(past), rope=mfb.Rope.from_freqs(f), Q=x[:, :4],
+                  Q_out=Qo, cu_seqlens=cu)
+    mfb.sync_status()
+    live = torch.cat([torch.arange(20), torch.arange(27, 60)]).cuda()
+    pos = torch.cat([torch.arange(3, 23), torch.arange(33)])
+    near_rotated(Qo[live], x[live][:, :4], pos, f, 64, False)
+    assert (Qo[20:27] == 9.0).all() and (Qo[60:] == 9.0).all()
+    at = torch.cat([slots(table, 16, 0, 3, 23), slots(table, 16, 2, 0, 33)])
+    near_rotated(c.K.view(-1, 2, 64)[at], x[live][:, 4:6], pos, f, 64, False)
+    keep = torch.ones(npages * 16, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    assert torch.equal(c.K.view(-1, 2, 64)[keep], K0.view(-1, 2, 64)[keep])
