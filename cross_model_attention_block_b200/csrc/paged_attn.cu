@@ -428,16 +428,17 @@ struct Bf16Body {
         o[i][1] += o[i][3];
       }
   }
-  // Hands every row to `sink`, pair of dims by pair of dims.
+  // Hands every row to `sink`.
   template <class Sink>
   __device__ __forceinline__ void put(int heads, const Sink& sink) const {
 #pragma unroll
     for (int n = 0; n < NR; ++n)
       if (row(n) < heads) {
-        const auto to = sink.row(row(n), m[n], l[n], lane % 4 == 0);
+        if (lane % 4 == 0) sink.stats(row(n), m[n], l[n]);
+        const float f = sink.factor(l[n]);
+        auto* to = sink.at(row(n)) + 2 * (lane % 4);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          to.store(i * 8 + 2 * (lane % 4), o[i][2 * n], o[i][2 * n + 1]);
+        for (int i = 0; i < D / 8; ++i) sink.store(to + i * 8, f, o[i][2 * n], o[i][2 * n + 1]);
       }
   }
 };
@@ -473,9 +474,15 @@ struct F32Body {
 
   __device__ __forceinline__ void begin(const T* Q, int heads) {
     __syncwarp();
-    for (int i = lane * 4; i < GT * D; i += 128)
-      *reinterpret_cast<float4*>(qs + i) =
-          i / D < heads ? *reinterpret_cast<const float4*>(Q + i) : make_float4(0, 0, 0, 0);
+    constexpr int kLoads = GT * D / 128;
+    float4 x[kLoads];  // all on their way before the first is stored
+#pragma unroll
+    for (int c = 0; c < kLoads; ++c) {
+      const int i = c * 128 + lane * 4;
+      x[c] = i / D < heads ? *reinterpret_cast<const float4*>(Q + i) : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < kLoads; ++c) *reinterpret_cast<float4*>(qs + c * 128 + lane * 4) = x[c];
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < GT; ++g)
@@ -597,14 +604,21 @@ struct F32Body {
     }
     __syncwarp();
   }
+  // The statistics a head a lane: their code, once a head in a row, would be
+  // fetched for longer than it runs.
   template <class Sink>
   __device__ __forceinline__ void put(int heads, const Sink& sink) const {
+    if (lane < heads) {
+      sink.stats(lane, cs[lane], ws[lane]);
+      qs[lane] = sink.factor(ws[lane]);
+    }
+    __syncwarp();
 #pragma unroll
     for (int g = 0; g < GT; ++g)
       if (g < heads) {
-        const auto to = sink.row(g, cs[g], ws[g], lane == 0);
+        auto* to = sink.at(g) + lane * NO;
 #pragma unroll
-        for (int n = 0; n < NO / 2; ++n) to.store(lane * NO + 2 * n, o[g][n].x, o[g][n].y);
+        for (int n = 0; n < NO / 2; ++n) sink.store(to + 2 * n, qs[g], o[g][n].x, o[g][n].y);
       }
   }
 };
@@ -619,40 +633,39 @@ __device__ __forceinline__ void store2(__nv_bfloat16* p, float a, float b) {
 }
 
 // A finished row: O and lse of query heads h0 .. of sequence s.
-template <typename T, int D>
+template <typename T_, int D>
 struct Finished {
+  using T = T_;
   const Params& p;
   int s, h0;
-  struct To {
-    T* o;
-    float inv;
-    bool none;  // nothing seen: zero, whatever was summed
-    __device__ __forceinline__ void store(int dim, float a, float b) const {
-      store2(o + dim, none ? 0.f : a * inv, none ? 0.f : b * inv);
-    }
-  };
-  __device__ __forceinline__ To row(int head, float m, float l, bool first) const {
-    const bool none = l == 0.f;
-    if (first && p.lse)
-      p.lse[int64_t(h0 + head) * p.nseq + s] = none ? -INFINITY : (m + log2f(l)) * kLn2;
-    return To{static_cast<T*>(p.O) + s * p.o_stride + int64_t(h0 + head) * D, 1.f / l, none};
+  __device__ __forceinline__ void stats(int head, float m, float l) const {
+    if (p.lse)
+      p.lse[int64_t(h0 + head) * p.nseq + s] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+  // of the sums; 0: nothing seen
+  __device__ __forceinline__ static float factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
+  __device__ __forceinline__ T* at(int head) const {
+    return static_cast<T*>(p.O) + s * p.o_stride + int64_t(h0 + head) * D;
+  }
+  // zero where nothing is seen, whatever was summed
+  __device__ __forceinline__ static void store(T* o, float f, float a, float b) {
+    store2(o, f == 0.f ? 0.f : a * f, f == 0.f ? 0.f : b * f);
   }
 };
 
 // A piece of a row: unnormalised sums [heads][D], maxima and sums of weights.
 template <int D>
 struct PieceAt {
+  using T = float;
   float* o;
   float2* ml;
-  struct To {
-    float* o;
-    __device__ __forceinline__ void store(int dim, float a, float b) const {
-      store2(o + dim, a, b);
-    }
-  };
-  __device__ __forceinline__ To row(int head, float m, float l, bool first) const {
-    if (first) ml[head] = make_float2(m, l);
-    return To{o + head * D};
+  __device__ __forceinline__ void stats(int head, float m, float l) const {
+    ml[head] = make_float2(m, l);
+  }
+  __device__ __forceinline__ static float factor(float) { return 1.f; }
+  __device__ __forceinline__ float* at(int head) const { return o + head * D; }
+  __device__ __forceinline__ static void store(float* o, float, float a, float b) {
+    store2(o, a, b);
   }
 };
 
@@ -676,9 +689,11 @@ struct Piece {  // running joint result; a lane owns D / 32 dims
 template <int D, class Sink>
 __device__ __forceinline__ void put_row(const Sink& sink, int head, const Piece<D>& x) {
   const int lane = threadIdx.x % 32;
-  const auto to = sink.row(head, x.m, x.l, lane == 0);
+  if (lane == 0) sink.stats(head, x.m, x.l);
+  const float f = sink.factor(x.l);
+  auto* to = sink.at(head) + lane * (D / 32);
 #pragma unroll
-  for (int i = 0; i < D / 32; i += 2) to.store(lane * (D / 32) + i, x.o[i], x.o[i + 1]);
+  for (int i = 0; i < D / 32; i += 2) sink.store(to + i, f, x.o[i], x.o[i + 1]);
 }
 
 // ------------------------------------------------------------ the main kernel
