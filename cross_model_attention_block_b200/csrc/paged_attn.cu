@@ -48,6 +48,8 @@ constexpr int kUnit = 16;      // keys of one unit
 // unit or two: 22.5 us with 2 to 5, 26.3 with 0).
 constexpr int kRowCost = 2;
 constexpr int kCtas = 148;     // one block per SM of a B200
+constexpr int kWarps = 8;      // of the main kernel's blocks
+constexpr int kThreads = kWarps * 32;
 // A row's reference m is not its running maximum: it moves when a logit lies
 // more than 2^kSlack above it, about once a row, and only then are the sums
 // rescaled.  Weights stay below 2^kSlack.
@@ -104,7 +106,7 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
 
 // The line is made of the rows' units, each row's behind kRowCost places that
 // stand for what a row costs besides its units (queries, sums, output).  It is
-// cut into kCtas << SHIFT equal runs: one for each warp of a block (SHIFT 2 or
+// cut into kCtas << SHIFT equal runs: one for each of a block's 8 warps (SHIFT
 // 3), or, the same cuts at the blocks, one for each block (SHIFT 0).
 template <int SHIFT>
 struct Cuts {
@@ -141,16 +143,14 @@ struct Walk {
   }
 };
 
-template <int THREADS>
 struct PlanSmem {
-  int64_t before[THREADS + 1];  // places of the sequences before thread t's
-  int64_t warp_sum[THREADS / 32];
+  int64_t before[kThreads + 1];  // places of the sequences before thread t's
+  int64_t warp_sum[kThreads / 32];
 };
 
 // Places of every thread's share of the sequences, added up over the block.
-template <int THREADS>
-__device__ __forceinline__ void plan_places(const Params& p, PlanSmem<THREADS>& sm, bool report) {
-  const int per = (p.nseq + THREADS - 1) / THREADS;
+__device__ __forceinline__ void plan_places(const Params& p, PlanSmem& sm, bool report) {
+  const int per = (p.nseq + kThreads - 1) / kThreads;
   const int s0 = min(int(threadIdx.x) * per, p.nseq), s1 = min(s0 + per, p.nseq);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
@@ -171,18 +171,17 @@ __device__ __forceinline__ void plan_places(const Params& p, PlanSmem<THREADS>& 
   __syncthreads();
   for (int w = 0; w < warp; ++w) sum += sm.warp_sum[w];
   sm.before[threadIdx.x] = sum - mine;
-  if (threadIdx.x == THREADS - 1) sm.before[THREADS] = sum;
+  if (threadIdx.x == kThreads - 1) sm.before[kThreads] = sum;
   __syncthreads();
 }
 
 // The place where the row before which `row` others come begins; rows of
 // sequences without keys count, but have no places.
-template <int THREADS>
-__device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem<THREADS>& sm,
+__device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem& sm,
                                                 int64_t row) {
   const int rows = p.Hkv * p.groups, s = int(row / rows);
-  if (s >= p.nseq) return sm.before[THREADS];
-  const int per = (p.nseq + THREADS - 1) / THREADS, t = s / per;
+  if (s >= p.nseq) return sm.before[kThreads];
+  const int per = (p.nseq + kThreads - 1) / kThreads, t = s / per;
   int64_t at = sm.before[t];
   for (int i = t * per; i < s; ++i) {
     const int n = span_of(p, i).n;
@@ -194,17 +193,16 @@ __device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem<
 
 // The first unit of the run of `n` places from place u on (the same in the
 // whole warp).
-template <int THREADS>
-__device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem<THREADS>& sm, int64_t u,
+__device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem& sm, int64_t u,
                                            int n) {
-  constexpr int kSub = THREADS / 32;
+  constexpr int kSub = kThreads / 32;
   const int lane = threadIdx.x % 32;
   const int t0 = (__popc(__ballot_sync(0xffffffffu, sm.before[lane * kSub] <= u)) - 1) * kSub;
   const bool below = lane < kSub && sm.before[t0 + lane % kSub] <= u;
   const int t = t0 - 1 + __popc(__ballot_sync(0xffffffffu, below));
   int64_t at = u - sm.before[t];
   Walk w;
-  w.s = t * ((p.nseq + THREADS - 1) / THREADS);
+  w.s = t * ((p.nseq + kThreads - 1) / kThreads);
   const int rows = p.Hkv * p.groups;
   while (true) {
     w.k = span_of(p, w.s);
@@ -282,7 +280,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 template <int D_, int HEADS>  // HEADS: 4, 8 or 16 query heads of a group at most
 struct Bf16Body {
   using T = __nv_bfloat16;
-  static constexpr int D = D_, kWarps = 8, kHeads = HEADS;
+  static constexpr int D = D_, kHeads = HEADS;
   static constexpr int kTile = kUnit * D * 2;
   // what the pieces of shared rows leave of 227 KB
   static constexpr int kStages = D == 128 ? (HEADS == 4 ? 3 : 2) : (HEADS == 16 ? 5 : 6);
@@ -451,15 +449,16 @@ struct Bf16Body {
 // operand of a packed FMA; then a lane owns D / 32 dims of every head.
 //
 // At few heads a group bound by memory (30 sequences of 300 to 3000 tokens, 8
-// heads over 8 of 128: 50 us, 73 % of the copy rate); from 8 on by the reads of
+// heads over 8 of 128: 49 us, 75 % of the copy rate); from 8 on by the reads of
 // shared memory, one of the queries for every two packed FMAs (32 heads over 4:
-// 40 us, 46 %; 16 over 1: 28 us, 17 %).
-template <int D_, int GT>  // GT: query heads of a group at most (even)
+// 40 us, 46 %; 40 over 2: 46 us, 20 %).  8 warps with a stage each hide more of
+// that than 4 warps with 3 and groups of 16 heads (40 over 2: 60 us).
+template <int D_, int GT>  // GT: query heads of a group at most (4 or 8)
 struct F32Body {
   using T = float;
-  static constexpr int D = D_, kWarps = D == 128 ? 4 : 8, kHeads = GT;
+  static constexpr int D = D_, kHeads = GT;
   static constexpr int kTile = kUnit * D * 4;
-  static constexpr int kStages = GT == 4 ? 3 : 2;
+  static constexpr int kStages = D == 128 ? 1 : GT == 4 ? 3 : 2;
   // queries [GT][D], weights [16 keys][GT][2], factors [GT]
   static constexpr int kScratch = GT * D * 4 + kUnit * GT * 8 + GT * 4 + 64;
   static constexpr int NO = D / 32;       // dims a lane owns
@@ -710,24 +709,23 @@ struct Cut {
 template <class Body>
 struct Layout {
   static constexpr int kStageBytes = 2 * Body::kTile;
-  static constexpr int kRing = Body::kWarps * Body::kStages * kStageBytes;
+  static constexpr int kRing = kWarps * Body::kStages * kStageBytes;
   static constexpr int kPiece = Body::kHeads * Body::D * 4;  // a row's sums
-  static constexpr int kOffPieces = kRing + Body::kWarps * Body::kScratch;
-  static constexpr int kBytes = kOffPieces + Body::kWarps * kPiece + 1024;  // 1024: alignment
+  static constexpr int kOffPieces = kRing + kWarps * Body::kScratch;
+  static constexpr int kBytes = kOffPieces + kWarps * kPiece + 1024;  // 1024: alignment
   static_assert(Body::kStages * kStageBytes >= kPiece);
 };
 
 template <class Body>
-__global__ void __launch_bounds__(Body::kWarps * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_paged_attn(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                  const Params p) {
   using T = typename Body::T;
   using S = Layout<Body>;
-  constexpr int D = Body::D, kWarps = Body::kWarps, kStages = Body::kStages;
-  constexpr int kThreads = kWarps * 32;
+  constexpr int D = Body::D, kStages = Body::kStages;
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  __shared__ PlanSmem<kThreads> plan;
+  __shared__ PlanSmem plan;
   __shared__ uint64_t bars[kWarps][kStages];
   // the pieces of rows that the block's warps share: [0] of the row a warp's run
   // begins in, [1] of the row it ends in
@@ -746,24 +744,24 @@ __global__ void __launch_bounds__(Body::kWarps * 32, 1)
   }
   // all before this ran beside the end of the launch before
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  plan_places<kThreads>(p, plan, blockIdx.x == 0);
+  plan_places(p, plan, blockIdx.x == 0);
   // the joining kernel may take its place now; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const Cuts<kWarps == 8 ? 3 : 2> cuts{plan.before[kThreads]};
+  const Cuts<3> cuts{plan.before[kThreads]};
   const int w0 = blockIdx.x * kWarps, w = w0 + warp;
   int64_t c0 = cuts.at(w0), u0 = cuts.at(w), u1 = cuts.at(w + 1);
   if (p.by_rows) {
     const int64_t rows = int64_t(p.nseq) * p.Hkv * p.groups;
-    c0 = place_of_row<kThreads>(p, plan, rows * blockIdx.x / kCtas);
-    const int64_t n = place_of_row<kThreads>(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0;
+    c0 = place_of_row(p, plan, rows * blockIdx.x / kCtas);
+    const int64_t n = place_of_row(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0;
     u0 = c0 + n * warp / kWarps;
     u1 = c0 + n * (warp + 1) / kWarps;
   }
   Walk at = {};
   bool begun = false;  // the row the run begins in is begun before it
   if (u1 > u0) {
-    at = find_place<kThreads>(p, plan, u0, int(u1 - u0));
+    at = find_place(p, plan, u0, int(u1 - u0));
     begun = at.g > 0;
   }
   Cut cut{-1, 0, 0, -1, 0, at.left > 0};
@@ -1082,19 +1080,21 @@ mf_status check(const mf_kv_cache* cache, const mf_paged_attn_desc* a) {
 }
 
 // Query heads of one KV head are taken together, up to what a warp's registers
-// hold (16); more are cut into even groups, each of which reads the keys again.
-int head_groups(const mf_kv_cache& c, int Hq) { return (Hq / c.Hkv + 15) / 16; }
-
-int warps_of(const mf_kv_cache& c) { return c.dt == MF_F32 && c.d == 128 ? 4 : 8; }
+// hold (16 for bf16, 8 for float32); more are cut into even groups, each of
+// which reads the keys again.
+int head_groups(const mf_kv_cache& c, int Hq) {
+  const int G = Hq / c.Hkv, most = c.dt == MF_BF16 ? 16 : 8;
+  return (G + most - 1) / most;
+}
 
 // Where the table has room for few places a block, blocks take whole rows:
 // nothing is left to join, and the second launch, 1 to 3 of the 7 to 10 us
 // that short rows take, is not made.  Few: those that its warps are through
 // with in that time (14 sequences of up to 215 tokens, 8 heads a KV head: 11.1
-// us with the second launch, 9.0 without; float32 with 10 heads a KV head and
-// 29 units a row: 15.5 with, 32 without).
-bool whole_rows(const mf_kv_cache& c, int gh, int groups) {
-  const int64_t few = warps_of(c) * (c.dt == MF_BF16 ? 4 : gh <= 4 ? 7 : 2);
+// us with the second launch, 9.0 without; float32, 19 of up to 491 tokens, 2
+// heads a KV head: 10.8 with, 15.1 without).
+bool whole_rows(const mf_kv_cache& c, int groups) {
+  const int64_t few = kWarps * (c.dt == MF_BF16 ? 4 : 2);
   const int64_t places = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) + kRowCost;
   const int64_t rows = int64_t(c.nseq) * c.Hkv * groups;
   return places <= few && (rows + kCtas - 1) / kCtas * places <= few;
@@ -1109,7 +1109,7 @@ size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   if (p) {
     p->groups = groups;
     p->gh = gh;
-    p->by_rows = whole_rows(c, gh, groups);
+    p->by_rows = whole_rows(c, groups);
     p->part_o = part_o;
     p->part_ml = part_ml;
     p->shared = shared;
@@ -1139,7 +1139,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(Body::kWarps * 32);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cfg.attrs = &attr;
@@ -1161,8 +1161,7 @@ cudaError_t launch_d(const Params& p, mf_dtype dt, const CUtensorMap& tk, const 
     return launch<Bf16Body<D, 16>>(p, tk, tv, st);
   }
   if (p.gh <= 4) return launch<F32Body<D, 4>>(p, tk, tv, st);
-  if (p.gh <= 8) return launch<F32Body<D, 8>>(p, tk, tv, st);
-  return launch<F32Body<D, 16>>(p, tk, tv, st);
+  return launch<F32Body<D, 8>>(p, tk, tv, st);
 }
 
 }  // namespace
