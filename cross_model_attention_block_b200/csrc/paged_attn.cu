@@ -1092,7 +1092,7 @@ int head_groups(const mf_kv_cache& c, int Hq) {
 // that short rows take, is not made.  Few: those that its warps are through
 // with in that time (14 sequences of up to 215 tokens, 8 heads a KV head: 11.1
 // us with the second launch, 9.0 without; float32, 19 of up to 491 tokens, 2
-// heads a KV head: 10.8 with, 15.1 without).
+// heads a KV head: 10.2 with, 15.1 without).
 bool whole_rows(const mf_kv_cache& c, int groups) {
   const int64_t few = kWarps * (c.dt == MF_BF16 ? 4 : 2);
   const int64_t places = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) + kRowCost;
