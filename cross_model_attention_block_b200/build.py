@@ -74,7 +74,7 @@ def build_marshal(force: bool = False) -> str:
         cmd += ["-isystem" if troot in i else "-I", i]
     tmp = MARSHAL + ".tmp"
     cmd += [MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(troot, "lib"), "-lc10", "-lc10_cuda",
-            "-ltorch_cpu", "-ltorch_python"]
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

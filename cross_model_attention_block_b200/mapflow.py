@@ -590,21 +590,27 @@ class KVCache:
     is what mapped_av reads."""
 
     def __init__(self, K, V, page_table):
-        if (K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or not K.is_contiguous()
-                or not V.is_contiguous()):
-            _refuse("K and V must be contiguous pools [npages, page_size, Hkv, d] of one dtype")
-        if (page_table.dtype != torch.int32 or page_table.dim() != 2
-                or not page_table.is_contiguous()):
-            _refuse("page_table must be a contiguous int32 tensor [nseq, max_pages_per_seq]")
+        if _fast is None:
+            load_library()
+        r = _fast.kv_cache(K, V, page_table)
+        if r is None:
+            if (K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype
+                    or not K.is_contiguous() or not V.is_contiguous()):
+                _refuse("K and V must be contiguous pools [npages, page_size, Hkv, d] of one "
+                        "dtype")
+            if (page_table.dtype != torch.int32 or page_table.dim() != 2
+                    or not page_table.is_contiguous()):
+                _refuse("page_table must be a contiguous int32 tensor "
+                        "[nseq, max_pages_per_seq]")
+            _dtype_code(K.dtype)
+            _refuse("a size of the pools or of the page table is past 32 bits")
         self.K, self.V, self.page_table = K, V, page_table
-        self.npages, self.page_size, self.Hkv, self.d = K.shape
-        self.nseq, self.max_pages = page_table.shape
-        self._desc = KvCacheDesc(K.data_ptr(), V.data_ptr(), page_table.data_ptr(), self.npages,
-                                 self.page_size, self.max_pages, self.nseq, self.Hkv, self.d,
-                                 _dtype_code(K.dtype))
-        self._addr = C.addressof(self._desc)
-        dev = K.get_device()
-        self._device = dev if V.get_device() == dev == page_table.get_device() else -1
+        (self.npages, self.page_size, self.Hkv, self.d, self.nseq, self.max_pages,
+         self._device, self._bytes, self._addr) = r
+
+    @property
+    def _desc(self):
+        return KvCacheDesc.from_buffer_copy(self._bytes)
 
     @classmethod
     def make(cls, npages, page_size, Hkv, d, dtype, page_table):
@@ -685,7 +691,8 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
         _refuse("lse must be a contiguous float32 tensor [Hq, nseq]")
     a = PagedAttnDesc(Hq, scale, band_bias, band_width, window,
                       len_add)
-    cr, ar = C.byref(cache._desc), C.byref(a)
+    c = cache._desc
+    cr, ar = C.byref(c), C.byref(a)
     nbytes = L.mf_paged_attn_workspace(cr, ar)
     if nbytes == 0:  # the call finds the same error and returns its status
         _check(L.mf_paged_attn(cr, ar, None, None, 0, None, 0, None, None, 0, None))
