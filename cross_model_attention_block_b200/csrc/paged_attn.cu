@@ -169,7 +169,11 @@ __device__ __forceinline__ void plan_places(const Params& p, PlanSmem& sm, bool 
   }
   if (lane == 31) sm.warp_sum[warp] = sum;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) sum += sm.warp_sum[w];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t x = sm.warp_sum[w];
+    if (w < warp) sum += x;
+  }
   sm.before[threadIdx.x] = sum - mine;
   if (threadIdx.x == kThreads - 1) sm.before[kThreads] = sum;
   __syncthreads();
@@ -177,18 +181,17 @@ __device__ __forceinline__ void plan_places(const Params& p, PlanSmem& sm, bool 
 
 // The place where the row before which `row` others come begins; rows of
 // sequences without keys count, but have no places.
-__device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem& sm,
-                                                int64_t row) {
-  const int rows = p.Hkv * p.groups, s = int(row / rows);
+__device__ __forceinline__ int64_t place_of_row(const Params& p, const PlanSmem& sm, int row) {
+  const int rows = p.Hkv * p.groups, s = row / rows;
   if (s >= p.nseq) return sm.before[kThreads];
   const int per = (p.nseq + kThreads - 1) / kThreads, t = s / per;
   int64_t at = sm.before[t];
   for (int i = t * per; i < s; ++i) {
     const int n = span_of(p, i).n;
-    at += n > 0 ? int64_t(n + kRowCost) * rows : 0;
+    at += n > 0 ? (n + kRowCost) * rows : 0;
   }
   const int n = span_of(p, s).n;
-  return at + (n > 0 ? (row - int64_t(s) * rows) * (n + kRowCost) : 0);
+  return at + (n > 0 ? (row - s * rows) * (n + kRowCost) : 0);
 }
 
 // The first unit of the run of `n` places from place u on (the same in the
@@ -750,13 +753,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const Cuts<3> cuts{plan.before[kThreads]};
   const int w0 = blockIdx.x * kWarps, w = w0 + warp;
-  int64_t c0 = cuts.at(w0), u0 = cuts.at(w), u1 = cuts.at(w + 1);
+  int64_t c0, u0, u1;
   if (p.by_rows) {
-    const int64_t rows = int64_t(p.nseq) * p.Hkv * p.groups;
+    const int rows = p.nseq * p.Hkv * p.groups;  // few: 32 bits
     c0 = place_of_row(p, plan, rows * blockIdx.x / kCtas);
-    const int64_t n = place_of_row(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0;
+    const int n = int(place_of_row(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0);
     u0 = c0 + n * warp / kWarps;
     u1 = c0 + n * (warp + 1) / kWarps;
+  } else {
+    c0 = cuts.at(w0);
+    u0 = cuts.at(w);
+    u1 = cuts.at(w + 1);
   }
   Walk at = {};
   bool begun = false;  // the row the run begins in is begun before it
@@ -1094,7 +1101,7 @@ int head_groups(const mf_kv_cache& c, int Hq) {
 // us with the second launch, 9.0 without; float32, 19 of up to 491 tokens, 2
 // heads a KV head: 10.2 with, 15.1 without).
 bool whole_rows(const mf_kv_cache& c, int groups) {
-  const int64_t few = kWarps * (c.dt == MF_BF16 ? 4 : 2);
+  const int64_t few = kWarps * (c.dt == MF_BF16 ? 4 : 2);  // so rows are few, too
   const int64_t places = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) + kRowCost;
   const int64_t rows = int64_t(c.nseq) * c.Hkv * groups;
   return places <= few && (rows + kCtas - 1) / kCtas * places <= few;
