@@ -446,33 +446,43 @@ struct Bf16Body {
 
 // ------------------------------------------------------ float32: packed FMAs
 //
-// Logits: lane (half, key) sums half of the dims for every head, the two
-// halves trade partial sums so that each ends with half of the heads (head
-// 2 i + half).  Weights go through shared memory, each twice in a row, the
-// operand of a packed FMA; then a lane owns D / 32 dims of every head.
+// Logits: a lane sums a quarter of the dims for two keys (k and k + 8) and every
+// head; the four lanes of a key trade partial sums so that each ends with a
+// quarter of the heads.  Weights go through shared memory; then a lane owns
+// D / 32 dims of every head.
 //
-// At few heads a group bound by memory (30 sequences of 300 to 3000 tokens, 8
-// heads over 8 of 128: 49 us, 75 % of the copy rate); from 8 on by the reads of
-// shared memory, one of the queries for every two packed FMAs (32 heads over 4:
-// 40 us, 46 %; 40 over 2: 46 us, 20 %).  8 warps with a stage each hide more of
-// that than 4 warps with 3 and groups of 16 heads (40 over 2: 60 us).
+// What bounds it: at few heads a group memory (30 sequences of 300 to 3000
+// tokens, 8 heads over 8 of 128: 47 us, 78 % of the copy rate); from 4 on the
+// reads of shared memory, 16 bytes a lane in 4 cycles however many lanes share
+// an address.  Two keys a lane halve those of the queries (40 heads over 2 of
+// 128: 41 us; 46 with a key and half of the dims a lane).  8 warps with a stage
+// each hide more than 4 warps with 3.
 template <int D_, int GT>  // GT: query heads of a group at most (4 or 8)
 struct F32Body {
   using T = float;
   static constexpr int D = D_, kHeads = GT;
   static constexpr int kTile = kUnit * D * 4;
   static constexpr int kStages = D == 128 ? 1 : GT == 4 ? 3 : 2;
-  // queries [GT][D], weights [16 keys][GT][2], factors [GT]
-  static constexpr int kScratch = GT * D * 4 + kUnit * GT * 8 + GT * 4 + 64;
-  static constexpr int NO = D / 32;       // dims a lane owns
+  static constexpr int kPieces = D / 16;     // 16-byte pieces of a quarter row
+  static constexpr int kQuarter = D / 4 + 4; // floats of a query's quarter: the four lie in
+                                             // different banks
+  static constexpr int NH = GT / 4;          // heads a lane ends with
+  // queries [GT][4][kQuarter], weights [16 keys][GT], factors [GT]
+  static constexpr int kScratch = (GT * 4 * kQuarter + kUnit * GT + GT) * 4;
+  static constexpr int NO = D / 32;          // dims a lane owns
 
-  int lane;
+  int lane, key, head;  // key: of the two, the first; head: the first it ends with
   float *qs, *ws, *cs;
   float2 o[GT][NO / 2];
-  float m[GT / 2], l[GT / 2];
+  float m[NH], l[NH];
 
   __device__ __forceinline__ F32Body(int lane_, void* scratch)
-      : lane(lane_), qs(static_cast<float*>(scratch)), ws(qs + GT * D), cs(ws + kUnit * GT * 2) {}
+      : lane(lane_),
+        key(lane_ % 8),
+        head((lane_ & 16 ? GT / 2 : 0) + (lane_ & 8 ? GT / 4 : 0)),
+        qs(static_cast<float*>(scratch)),
+        ws(qs + GT * 4 * kQuarter),
+        cs(ws + kUnit * GT) {}
 
   __device__ __forceinline__ void begin(const T* Q, int heads) {
     __syncwarp();
@@ -484,74 +494,104 @@ struct F32Body {
       x[c] = i / D < heads ? *reinterpret_cast<const float4*>(Q + i) : make_float4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int c = 0; c < kLoads; ++c) *reinterpret_cast<float4*>(qs + c * 128 + lane * 4) = x[c];
+    for (int c = 0; c < kLoads; ++c) {
+      const int i = c * 128 + lane * 4;
+      *reinterpret_cast<float4*>(qs + i / (D / 4) * kQuarter + i % (D / 4)) = x[c];
+    }
     __syncwarp();
 #pragma unroll
     for (int g = 0; g < GT; ++g)
 #pragma unroll
       for (int c = 0; c < NO / 2; ++c) o[g][c] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < GT / 2; ++i) {
+    for (int i = 0; i < NH; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
   }
 
   __device__ __forceinline__ void step(const Params& p, char* K, char* V, int j0, const Span& k) {
-    const int key = lane % 16, half = lane / 16;
-    float x[GT / 2];
+    const int quarter = lane / 8;
+    float x[GT][2];
     {
-      float2 acc[GT];
+      float2 acc[GT][2];
 #pragma unroll
-      for (int g = 0; g < GT; ++g) acc[g] = make_float2(0.f, 0.f);
+      for (int g = 0; g < GT; ++g) acc[g][0] = acc[g][1] = make_float2(0.f, 0.f);
 #pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {  // 16-byte pieces of this half's dims
-        const int piece = half * (D / 8) + i;
-        const float4 kv = *reinterpret_cast<const float4*>(
-            K + (piece / 8) * 2048 + key * 128 + (((piece % 8) ^ (key % 8)) << 4));
+      for (int i = 0; i < kPieces; ++i) {
+        const int piece = quarter * kPieces + i;
+        const char* at = K + (piece / 8) * 2048 + key * 128 + (((piece % 8) ^ key) << 4);
+        const float4 k0 = *reinterpret_cast<const float4*>(at);
+        const float4 k1 = *reinterpret_cast<const float4*>(at + 8 * 128);
 #pragma unroll
         for (int g = 0; g < GT; ++g) {
-          const float4 qv = *reinterpret_cast<const float4*>(qs + g * D + piece * 4);
-          acc[g] = ffma2(make_float2(kv.x, kv.y), make_float2(qv.x, qv.y), acc[g]);
-          acc[g] = ffma2(make_float2(kv.z, kv.w), make_float2(qv.z, qv.w), acc[g]);
+          const float4 q = *reinterpret_cast<const float4*>(qs + (g * 4 + quarter) * kQuarter +
+                                                            i * 4);
+          const float2 qa = make_float2(q.x, q.y), qb = make_float2(q.z, q.w);
+          acc[g][0] = ffma2(make_float2(k0.x, k0.y), qa, acc[g][0]);
+          acc[g][0] = ffma2(make_float2(k0.z, k0.w), qb, acc[g][0]);
+          acc[g][1] = ffma2(make_float2(k1.x, k1.y), qa, acc[g][1]);
+          acc[g][1] = ffma2(make_float2(k1.z, k1.w), qb, acc[g][1]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < GT / 2; ++i) {
-        const float a = acc[2 * i].x + acc[2 * i].y, b = acc[2 * i + 1].x + acc[2 * i + 1].y;
-        const float other = __shfl_xor_sync(0xffffffffu, half ? a : b, 16);
-        x[i] = ((half ? b : a) + other) * p.scale2;
-      }
+      for (int g = 0; g < GT; ++g)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) x[g][n] = acc[g][n].x + acc[g][n].y;
     }
-    const int j = j0 + key;
-    const bool seen = j >= k.lo && j < k.len;
-    const float bias = j >= k.band_lo ? p.bias2 : 0.f;
+    // the quarters' sums: half of the heads to the lane 16 away, then a quarter
+    // to the one 8 away
+    const auto trade = [&](int half, int mask) {
+      const bool up = lane & mask;
+#pragma unroll
+      for (int g = 0; g < GT / 2; ++g)
+        if (g < half)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float other =
+                __shfl_xor_sync(0xffffffffu, up ? x[g][n] : x[g + half][n], mask);
+            x[g][n] = (up ? x[g + half][n] : x[g][n]) + other;
+          }
+    };
+    trade(GT / 2, 16);
+    trade(GT / 4, 8);
+
+    float mx[NH];
     bool up = false;
-    float mx[GT / 2];
 #pragma unroll
-    for (int i = 0; i < GT / 2; ++i) {
-      x[i] = seen ? x[i] + bias : -INFINITY;
-      mx[i] = x[i];
+    for (int i = 0; i < NH; ++i) {
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1)
+      for (int n = 0; n < 2; ++n) {
+        const int j = j0 + key + 8 * n;
+        x[i][n] = j >= k.lo && j < k.len
+                      ? fmaf(x[i][n], p.scale2, j >= k.band_lo ? p.bias2 : 0.f)
+                      : -INFINITY;
+      }
+      mx[i] = fmaxf(x[i][0], x[i][1]);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1)
         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
       up |= mx[i] > m[i] + kSlack;
     }
     const bool any_up = __any_sync(0xffffffffu, up);
     if (any_up) {
 #pragma unroll
-      for (int i = 0; i < GT / 2; ++i) {
+      for (int i = 0; i < NH; ++i) {
         const Join f(m[i], mx[i]);
         m[i] = f.m;
         l[i] *= f.ca;
-        if (key == 0) cs[2 * i + half] = f.ca;
+        if (key == 0) cs[head + i] = f.ca;
       }
     }
 #pragma unroll
-    for (int i = 0; i < GT / 2; ++i) {
-      const float w = ex2(x[i] - (m[i] == -INFINITY ? 0.f : m[i]));
-      l[i] += w;
-      *reinterpret_cast<float2*>(ws + (key * GT + 2 * i + half) * 2) = make_float2(w, w);
+    for (int i = 0; i < NH; ++i) {
+      const float ref = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float w = ex2(x[i][n] - ref);
+        l[i] += w;
+        ws[(key + 8 * n) * GT + head + i] = w;
+      }
     }
     __syncwarp();
     if (any_up) {
@@ -581,12 +621,14 @@ struct F32Body {
         v[0] = *reinterpret_cast<const float2*>(at);
       }
 #pragma unroll
-      for (int g = 0; g < GT; g += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(ws + (r * GT + g) * 2);
+      for (int g = 0; g < GT; g += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(ws + r * GT + g);
 #pragma unroll
         for (int n = 0; n < NO / 2; ++n) {
-          o[g][n] = ffma2(make_float2(w.x, w.y), v[n], o[g][n]);
-          o[g + 1][n] = ffma2(make_float2(w.z, w.w), v[n], o[g + 1][n]);
+          o[g][n] = ffma2(make_float2(w.x, w.x), v[n], o[g][n]);
+          o[g + 1][n] = ffma2(make_float2(w.y, w.y), v[n], o[g + 1][n]);
+          o[g + 2][n] = ffma2(make_float2(w.z, w.z), v[n], o[g + 2][n]);
+          o[g + 3][n] = ffma2(make_float2(w.w, w.w), v[n], o[g + 3][n]);
         }
       }
     }
@@ -596,12 +638,12 @@ struct F32Body {
   // Completes the sums over the warp's lanes; every lane gets all heads' m and l.
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int i = 0; i < GT / 2; ++i) {
+    for (int i = 0; i < NH; ++i) {
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-      if (lane % 16 == 0) {
-        cs[2 * i + lane / 16] = m[i];
-        ws[2 * i + lane / 16] = l[i];
+      for (int d = 4; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      if (key == 0) {
+        cs[head + i] = m[i];
+        ws[head + i] = l[i];
       }
     }
     __syncwarp();
