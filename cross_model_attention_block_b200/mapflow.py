@@ -95,7 +95,7 @@ _fast = None  # the decode calls' marshalling in C++ (csrc_py/marshal.cpp)
 
 def load_library(path: str = LIB_PATH):
     """Load libmapflow.so and declare its signatures (no GPU needed)."""
-    global _lib, _fast
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -149,14 +149,7 @@ def load_library(path: str = LIB_PATH):
         f = getattr(L, name)
         f.restype = res
         f.argtypes = args
-    try:
-        from . import _marshal
-    except ImportError as e:
-        raise RuntimeError("_marshal.so is missing or does not fit this torch: build it with "
-                           "`python -m cross_model_attention_block_b200.build`") from e
-    _marshal.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in (
-        "mf_rope", "mf_kv_append", "mf_paged_attn", "mf_paged_attn_workspace")))
-    _lib, _fast = L, _marshal
+    _lib = L
     return L
 
 
@@ -455,6 +448,20 @@ def _require(ok, msg):
 # returns None where one is not of the plain kind; the checks below then say what is
 # wrong, or the call is made from here (on another device than the current one).
 
+def _load_fast():
+    global _fast
+    L = load_library()
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError("_marshal.so is missing or does not fit this torch: build it with "
+                           "`python -m cross_model_attention_block_b200.build --force`") from e
+    _marshal.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in (
+        "mf_rope", "mf_kv_append", "mf_paged_attn", "mf_paged_attn_workspace")))
+    _fast = _marshal
+    return _fast
+
+
 def _made(r):
     """The result of a call that _fast made: its outputs, unless it is a status."""
     if type(r) is int:
@@ -553,9 +560,8 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     start[s] + t - cu_seqlens[s]; without cu_seqlens, start [ntok] holds every token's
     own position.  backward=True takes gradients of the outputs to those of the inputs.
     Q_out may be Q, and K_out may be K."""
-    if _fast is None:
-        load_library()
-    r = _fast.rope(rp._addr, rp.phases, Q, K, start, cu_seqlens, Q_out, K_out, backward)
+    f = _fast or _load_fast()
+    r = f.rope(rp._addr, rp.phases, Q, K, start, cu_seqlens, Q_out, K_out, backward)
     if r is not None:
         return _made(r)
     _require(start is not None or cu_seqlens is not None, "start or cu_seqlens must be given")
@@ -590,9 +596,7 @@ class KVCache:
     is what mapped_av reads."""
 
     def __init__(self, K, V, page_table):
-        if _fast is None:
-            load_library()
-        r = _fast.kv_cache(K, V, page_table)
+        r = (_fast or _load_fast()).kv_cache(K, V, page_table)
         if r is None:
             if (K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype
                     or not K.is_contiguous() or not V.is_contiguous()):
@@ -627,11 +631,9 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     without Q).  cu_seqlens [nseq + 1]: the new tokens of every sequence; None: one each.
     A negative length marks a padding sequence, whose rows are left as they were.
     `lens` itself is not changed."""
-    if _fast is None:
-        load_library()
-    r = _fast.kv_append(cache._addr, cache._device, K, V, lens,
-                        None if rope is None else rope._addr,
-                        None if rope is None else rope.phases, Q, Q_out, cu_seqlens)
+    f = _fast or _load_fast()
+    r = f.kv_append(cache._addr, cache._device, K, V, lens, None if rope is None else rope._addr,
+                    None if rope is None else rope.phases, Q, Q_out, cu_seqlens)
     if r is not None:
         return None if r is True else _made(r)
     _require(K.dim() == 3, "K must be [ntok, Hkv, d]")
@@ -650,7 +652,7 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     else:
         _require(Q_out is None, "Q_out without Q")
     _call(cache.K.get_device(), (cache.V, cache.page_table, K, V, lens, Q, Q_out, cu_seqlens,
-                           None if rope is None else rope.phases),
+                                 None if rope is None else rope.phases),
           load_library().mf_kv_append, C.byref(cache._desc),
           None if rope is None else C.byref(rope._desc), C.byref(b), K.data_ptr(), ks,
           V.data_ptr(), vs, *qargs)
@@ -668,9 +670,8 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
     `workspace` may be a uint8 device tensor reused across calls (one per call in flight)."""
     if scale is None:
         scale = cache.d ** -0.5
-    if _fast is None:
-        load_library()
-    r = _fast.paged_attn(cache._addr, cache._device, Q, lens, O, lse, workspace, len_add, scale,
+    f = _fast or _load_fast()
+    r = f.paged_attn(cache._addr, cache._device, Q, lens, O, lse, workspace, len_add, scale,
                          band_bias, band_width, window)
     if r is not None:
         return _made(r)
