@@ -15,9 +15,9 @@
 //
 //  * A unit is 16 keys and values of one KV head (16 tokens never straddle a
 //    page).  The units of all rows (sequence, KV head, group of query heads),
-//    laid end to end, are cut into equal runs, one per warp of a fixed grid;
-//    every block finds the cuts itself from `lens`, so the host needs no
-//    lengths and a captured call follows them.
+//    laid end to end, are cut into runs, one per block and in equal parts one
+//    per warp; every block finds the cuts itself from `lens`, so the host needs
+//    no lengths and a captured call follows them.
 //  * A warp runs alone: it copies its units by TMA into its own ring of
 //    shared memory (one box of 16 tokens x 1 head for K, one for V, 128-byte
 //    swizzled) and waits on its own barriers; no block-wide step in the loop.
@@ -28,10 +28,8 @@
 //    the order of the sums depend on the lengths alone.
 //
 // Measured (bf16, d 128, 32 heads over 8, pages of 16): 64 sequences of 1 K to
-// 16 K tokens, 1.39 GB, 226 us (6.2 TB/s; what is left is that SMs do not read
-// at one speed: the first are done at 170 us, the last at 215); 32 K tokens 31
-// us, of which 2 to find the cuts, 21 at 6.4 TB/s and 6 to join; 1 K tokens 9.4
-// us, all of it latency.
+// 16 K tokens, 1.39 GB, 217 us (6.4 TB/s); 32 K tokens 31 us, of which 2 to find
+// the cuts, 21 at 6.4 TB/s and 6 to join; 1 K tokens 9.2 us, all of it latency.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -49,6 +47,14 @@ constexpr int kUnit = 16;      // keys of one unit
 constexpr int kRowCost = 2;
 constexpr int kCtas = 148;     // one block per SM of a B200
 constexpr int kWarps = 8;      // of the main kernel's blocks
+// A line of kLarge places a block leaves 1 / kRest of itself to kExtra more
+// blocks.  Measured, 64 sequences of 1 K to 16 K tokens: 215 us with 8, 219 with
+// 6 or with half as many blocks, 224 without; batches of 540 and 600 places a
+// block lose (97 -> 103 us) and break even (111 -> 112), of 1000 and 1280 gain
+// (172 -> 167, 211 -> 205).
+constexpr int kExtra = 2 * kCtas;
+constexpr int kRest = 8;
+constexpr int kLarge = 800;
 constexpr int kThreads = kWarps * 32;
 // A row's reference m is not its running maximum: it moves when a logit lies
 // more than 2^kSlack above it, about once a row, and only then are the sums
@@ -72,6 +78,7 @@ struct Params {
   int nseq, Hq, Hkv, G, page_size, max_pages, len_add, band, window;
   int groups, gh;  // groups of query heads per KV head, heads of a group
   bool by_rows;    // blocks take whole rows
+  int extra;       // blocks past the first kCtas
   float scale2, bias2;  // times log2 e
   // workspace: pieces of the rows that blocks share (two per block: of the row
   // its run begins in and of the row it ends in); entry b of `shared`: the row
@@ -106,22 +113,39 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
 
 // The line is made of the rows' units, each row's behind kRowCost places that
 // stand for what a row costs besides its units (queries, sums, output).  It is
-// cut into kCtas << SHIFT equal runs: one for each of a block's 8 warps (SHIFT
-// 3), or, the same cuts at the blocks, one for each block (SHIFT 0).
-template <int SHIFT>
+// cut into a run for every block, and that into equal runs for its warps.  The
+// first kCtas blocks, which fill the GPU, share `head` places evenly, and
+// `extra` blocks what is left.
+//
+// SMs do not read at one speed: those that share their path to L2 with more
+// others are slower (with equal runs the first is done after 170 us, most after
+// 190, the last after 215).  So a large line leaves a part to short runs, of
+// blocks that the hardware starts where others have ended.
 struct Cuts {
-  int64_t total;
-  // first place of run w
-  __device__ __forceinline__ int64_t at(int w) const {
-    const uint64_t x = uint64_t(total) * uint32_t(w);
-    return int64_t((x >> 32 ? x / kCtas : uint32_t(x) / uint32_t(kCtas)) >> SHIFT);
+  int64_t total, head;
+  int extra;
+  __device__ __forceinline__ static int64_t part(int64_t n, int i, uint32_t of) {
+    const uint64_t x = uint64_t(n) * uint32_t(i);
+    return int64_t(x >> 32 ? x / of : uint32_t(x) / of);
   }
-  // the run that holds place u
+  __device__ __forceinline__ static int which(int64_t n, int64_t u, uint32_t of) {
+    const uint64_t x = uint64_t(u + 1) * of - 1;
+    return x >> 32 ? int(x / uint64_t(n)) : int(uint32_t(x) / uint32_t(n));
+  }
+  // first place of block b
+  __device__ __forceinline__ int64_t at(int b) const {
+    return b <= kCtas ? part(head, b, kCtas) : head + part(total - head, b - kCtas, extra);
+  }
+  // the block that holds place u
   __device__ __forceinline__ int holder(int64_t u) const {
-    const uint64_t x = uint64_t(u + 1) * uint32_t(kCtas << SHIFT) - 1;
-    return x >> 32 ? int(x / uint64_t(total)) : int(uint32_t(x) / uint32_t(total));
+    return u < head ? which(head, u, kCtas) : kCtas + which(total - head, u - head, extra);
   }
 };
+
+__device__ __forceinline__ Cuts cuts_of(const Params& p, int64_t total) {
+  const bool large = p.extra > 0 && total >= int64_t(kCtas) * kLarge;
+  return Cuts{total, large ? total - total / kRest : total, p.extra};
+}
 
 // A place in the line: a unit, and how much of the run is left from there.
 struct Walk {
@@ -793,20 +817,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the joining kernel may take its place now; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const Cuts<3> cuts{plan.before[kThreads]};
-  const int w0 = blockIdx.x * kWarps, w = w0 + warp;
-  int64_t c0, u0, u1;
+  const Cuts cuts = cuts_of(p, plan.before[kThreads]);
+  int64_t c0, c1;  // the block's run
   if (p.by_rows) {
     const int rows = p.nseq * p.Hkv * p.groups;  // few: 32 bits
     c0 = place_of_row(p, plan, rows * blockIdx.x / kCtas);
-    const int n = int(place_of_row(p, plan, rows * (blockIdx.x + 1) / kCtas) - c0);
-    u0 = c0 + n * warp / kWarps;
-    u1 = c0 + n * (warp + 1) / kWarps;
+    c1 = place_of_row(p, plan, rows * (blockIdx.x + 1) / kCtas);
   } else {
-    c0 = cuts.at(w0);
-    u0 = cuts.at(w);
-    u1 = cuts.at(w + 1);
+    c0 = cuts.at(blockIdx.x);
+    c1 = cuts.at(blockIdx.x + 1);
   }
+  const int64_t u0 = c0 + (c1 - c0) * warp / kWarps, u1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
   Walk at = {};
   bool begun = false;  // the row the run begins in is begun before it
   if (u1 > u0) {
@@ -876,16 +897,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- while they are on their way: the row to join that the block begins in
   if (!p.by_rows && lane == 0) {
     if (u0 == c0 && u1 > u0) {
-      const Cuts<0> blocks{cuts.total};
       const int64_t row = u0 - at.g;  // its first unit, if that is before the block
       const bool full = cuts.total >= kCtas;  // else blocks hold a place or none
       Shared x{at.s, at.r, 0, -1};
-      if (begun && row >= (full ? blocks.at(blockIdx.x - 1) : u0 - 1)) {
-        x.v0 = full ? blockIdx.x - 1 : blocks.holder(row);
-        x.v1 = blocks.holder(row + at.k.n - 1);
+      if (begun && row >= (full ? cuts.at(blockIdx.x - 1) : u0 - 1)) {
+        x.v0 = full ? blockIdx.x - 1 : cuts.holder(row);
+        x.v1 = cuts.holder(row + at.k.n - 1);
       }
       p.shared[blockIdx.x] = x;
-    } else if (warp == 0 && cuts.at(w0 + kWarps) == c0) {  // an empty block
+    } else if (warp == 0 && c1 == c0) {  // an empty block
       p.shared[blockIdx.x] = Shared{0, 0, 0, -1};
       for (int i = 0; i < 2 * p.gh; ++i)
         p.part_ml[int64_t(2) * blockIdx.x * p.gh + i] = make_float2(-INFINITY, 0.f);
@@ -1001,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   // sequences without keys
-  for (int s = blockIdx.x; s < p.nseq; s += kCtas) {
+  for (int s = blockIdx.x; s < p.nseq; s += gridDim.x) {
     if (span_of(p, s).n > 0) continue;
     for (int i = threadIdx.x; i < p.Hq * (D / 2); i += kThreads)
       store2(static_cast<T*>(p.O) + s * p.o_stride + 2 * i, 0.f, 0.f);
@@ -1067,7 +1087,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // lane i: the boundary before block blockIdx.x * 8 + i
   Shared row{0, 0, 0, -1};
-  if (lane < kJoinWarps && w < kCtas) row = p.shared[w];
+  if (lane < kJoinWarps && w < kCtas + p.extra) row = p.shared[w];
   const bool split = row.v0 <= row.v1 && head < min(p.gh, p.G - row.r % p.groups * p.gh);
   const unsigned mine = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 < kJoinAlone);
   unsigned shared = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 >= kJoinAlone);
@@ -1149,16 +1169,24 @@ bool whole_rows(const mf_kv_cache& c, int groups) {
   return places <= few && (rows + kCtas - 1) / kCtas * places <= few;
 }
 
+// Blocks past the first kCtas, where the table has room for a large line.
+int extra_blocks(const mf_kv_cache& c, int groups) {
+  const int64_t units = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit);
+  return units * c.nseq * c.Hkv * groups >= int64_t(kCtas) * kLarge ? kExtra : 0;
+}
+
 size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
   const int groups = head_groups(c, Hq), G = Hq / c.Hkv, gh = (G + groups - 1) / groups;
+  const int extra = extra_blocks(c, groups), blocks = kCtas + extra;
   Carve k(ws);
-  float* part_o = k.take<float>(size_t(2 * kCtas) * gh * c.d);
-  float2* part_ml = k.take<float2>(size_t(2 * kCtas) * gh);
-  Shared* shared = k.take<Shared>(kCtas);
+  float* part_o = k.take<float>(size_t(2 * blocks) * gh * c.d);
+  float2* part_ml = k.take<float2>(size_t(2 * blocks) * gh);
+  Shared* shared = k.take<Shared>(blocks);
   if (p) {
     p->groups = groups;
     p->gh = gh;
     p->by_rows = whole_rows(c, groups);
+    p->extra = extra;
     p->part_o = part_o;
     p->part_ml = part_ml;
     p->shared = shared;
@@ -1187,7 +1215,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas);
+  cfg.gridDim = dim3(kCtas + p.extra);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
@@ -1195,7 +1223,7 @@ cudaError_t launch(const Params& p, const CUtensorMap& tk, const CUtensorMap& tv
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, k_paged_attn<Body>, tk, tv, p);
   if (e != cudaSuccess || p.by_rows) return e;
-  cfg.gridDim = dim3((kCtas + kJoinWarps - 1) / kJoinWarps, p.gh);
+  cfg.gridDim = dim3((kCtas + p.extra + kJoinWarps - 1) / kJoinWarps, p.gh);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, k_paged_join<typename Body::T, Body::D>, p);

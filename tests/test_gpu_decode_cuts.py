@@ -68,6 +68,29 @@ def test_totals_around_the_numbers_of_blocks_and_warps(dt, total):
         check_attention(c, lengths, Q, O, lse, 64 ** -0.5)
 
 
+@pytest.mark.parametrize("dt,Hq,Hkv,d,rows", [(BF, 16, 8, 64, 8), (BF, 64, 2, 128, 4),
+                                              (F32, 33, 1, 128, 5), (F32, 8, 8, 64, 8)])
+@pytest.mark.parametrize("few", [False, True], ids=["spread", "few_long"])
+def test_lines_long_enough_for_more_blocks(dt, Hq, Hkv, d, rows, few):
+    """Calls of 148 * 800 sixteens of keys (a row counts two besides) and more are cut for more
+    blocks than fill the GPU; one sixteen fewer, and short ones behind the same table, are not."""
+    need = 148 * 800 // rows  # sixteens and twos that each of a sequence's rows has to bring
+    rest = [16 * (need - 3) // 2 - 16, 16 * (need + 1) // 4] if few else mixed(7, 150, 4000)
+    used = sum((n + 15) // 16 + 2 for n in rest if n > 0)
+    lengths = rest + [16 * (need - used - 2)]
+    c = filled_cache(lengths, 16, Hkv, d, dt, 60)
+    Q = randn((len(lengths), Hq, d), dt, 61)
+    for last in (lengths[-1], lengths[-1] - 16, 5):
+        lengths[-1] = last
+        O, lse = mfb.paged_attn(c, Q, i32(lengths))
+        mfb.sync_status()
+        check_attention(c, lengths, Q, O, lse, d ** -0.5)
+    lengths = [min(n, 40) for n in lengths]
+    O, lse = mfb.paged_attn(c, Q, i32(lengths))
+    mfb.sync_status()
+    check_attention(c, lengths, Q, O, lse, d ** -0.5)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_many_sequences(dt):
     """More sequences than a block has threads, empty ones among them, windows inside."""
