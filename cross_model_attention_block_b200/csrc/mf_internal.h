@@ -75,9 +75,10 @@ cudaError_t launch_extract_tc(const mf_attn_desc& d, const Sizes& sz, const QbRa
                               cudaStream_t st);
 
 // Tensor map of a bf16 tensor (rank <= 5; strides of dims 1.. in bytes;
-// swizzle_bytes 0, 32, 64 or 128).
+// swizzle_bytes 0, 32, 64 or 128; l2_bytes, 128 or 256: what a miss in L2 brings).
 cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                           const uint64_t* strides_bytes, const uint32_t* box, int swizzle_bytes);
+                           const uint64_t* strides_bytes, const uint32_t* box, int swizzle_bytes,
+                           int l2_bytes = 256);
 
 bool mapped_av_tc_supported(const mf_attn_desc& d, int Hr, const mf_v_desc& v);
 // Workspace of the tensor-core fused kernel: per-sequence 16-key-group prefix

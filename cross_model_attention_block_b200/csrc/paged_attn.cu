@@ -75,8 +75,9 @@ struct Params {
   const int32_t* page_table;
   const int32_t* lens;
   int64_t q_stride, o_stride, npages;
-  int nseq, Hq, Hkv, G, page_size, max_pages, len_add, band, window;
-  int groups, gh;  // groups of query heads per KV head, heads of a group
+  int nseq, Hq, page_size, max_pages, len_add, band, window;
+  int Hkv, G, groups, gh;  // as in Rows
+  bool pair;
   bool by_rows;    // blocks take whole rows
   int extra;       // blocks past the first kCtas
   float scale2, bias2;  // times log2 e
@@ -304,13 +305,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int D_, int HEADS>  // HEADS: 4, 8 or 16 query heads of a group at most
+// HEADS: 4, 8 or 16 query heads of a row at most.  PAIR: a row has two KV heads,
+// whose 64 dims lie side by side, and the query heads of both; the products are
+// taken with both, and a query head keeps the one that is its own.
+template <int D_, int HEADS, bool PAIR = false>
 struct Bf16Body {
   using T = __nv_bfloat16;
   static constexpr int D = D_, kHeads = HEADS;
-  static constexpr int kTile = kUnit * D * 2;
+  static constexpr int KD = PAIR ? 2 * D : D;  // dims of a key as it is copied
+  static constexpr int kTile = kUnit * KD * 2;
   // what the pieces of shared rows leave of 227 KB
-  static constexpr int kStages = D == 128 ? (HEADS == 4 ? 3 : 2) : (HEADS == 16 ? 5 : 6);
+  static constexpr int kStages = KD == 64 ? (HEADS == 16 ? 5 : 6) : HEADS * D <= 512 ? 3 : 2;
   static constexpr int kScratch = 0;  // bytes of shared memory per warp besides the ring
   static constexpr bool kPacked = HEADS <= 8;
   static constexpr int NR = kPacked ? 1 : 2;  // rows of the product a thread holds
@@ -318,8 +323,9 @@ struct Bf16Body {
 
   int lane;
   uint32_t q[KS][2 * NR];
-  float o[D / 8][4];
+  float o[KD / 8][4];
   float m[NR], l[NR];
+  bool second[NR];  // PAIR: the row's KV head is the second
 
   __device__ __forceinline__ Bf16Body(int lane_, void*) : lane(lane_) {}
 
@@ -329,6 +335,7 @@ struct Bf16Body {
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       const bool live = row(n) < heads;
+      second[n] = PAIR && row(n) >= heads / 2;
       const T* x = Q + (live ? row(n) : 0) * D + 2 * (lane % 4);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -339,7 +346,7 @@ struct Bf16Body {
       l[n] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < KD / 8; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   }
@@ -347,25 +354,26 @@ struct Bf16Body {
   // One unit: keys j0 .. j0+15 at `K`, values at `V`; keys outside [lo, len)
   // take no part, those from band_lo on get the bias.
   __device__ __forceinline__ void step(const Params& p, char* K, char* V, int j0, const Span& k) {
-    float s[2][4] = {};
+    float s[2][4] = {}, s2[2][4] = {};
     {
       const int r = (lane / 16) * 8 + lane % 8;
       const uint32_t base = smem_u32(K) + r * 128;
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
+      for (int i = 0; i < KD / 16; ++i) {
         const int c = 2 * i + (lane / 8) % 2;
         uint32_t b[4];
         ldsm4(b, base + (c / 8) * 2048 + (((c % 8) ^ (r % 8)) << 4));
-        const uint32_t* a = q[i];
+        const uint32_t* a = q[i % KS];
         const uint32_t a1 = kPacked ? 0u : a[1], a3 = kPacked ? 0u : a[NR + 1];
-        mma16816(s[0], a[0], a1, a[NR], a3, b[0], b[1]);
-        mma16816(s[1], a[0], a1, a[NR], a3, b[2], b[3]);
+        float(&to)[2][4] = i < KS ? s : s2;
+        mma16816(to[0], a[0], a1, a[NR], a3, b[0], b[1]);
+        mma16816(to[1], a[0], a1, a[NR], a3, b[2], b[3]);
       }
     }
     const bool inside = j0 >= k.lo && j0 + kUnit <= k.len;
     const bool band = j0 + kUnit > k.band_lo;
     if (!inside) {  // what lies outside may hold anything: zero times it is not zero
-      constexpr int kRow = D * 2 / 16;
+      constexpr int kRow = KD * 2 / 16;
       for (int i = lane; i < kUnit * kRow; i += 32) {
         const int r = i / kRow, c = i % kRow;
         if (j0 + r < k.lo || j0 + r >= k.len)
@@ -380,7 +388,8 @@ struct Bf16Body {
     for (int n = 0; n < NR; ++n) {
       float x[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = s[c / 2][2 * n + c % 2] * p.scale2;
+      for (int c = 0; c < 4; ++c)
+        x[c] = (PAIR && second[n] ? s2[c / 2][2 * n + c % 2] : s[c / 2][2 * n + c % 2]) * p.scale2;
       if (band || !inside) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -397,7 +406,7 @@ struct Bf16Body {
         m[n] = f.m;
         l[n] *= f.ca;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < KD / 8; ++i) {
           o[i][2 * n] *= f.ca;
           o[i][2 * n + 1] *= f.ca;
           if (kPacked) {
@@ -422,7 +431,7 @@ struct Bf16Body {
       const uint32_t base = smem_u32(V) + r * 128;
       constexpr int n = NR - 1;
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
+      for (int i = 0; i < KD / 16; ++i) {
         const int c = 2 * i + lane / 16;
         uint32_t v[4];
         ldsm4_t(v, base + (c / 8) * 2048 + (((c % 8) ^ (r % 8)) << 4));
@@ -448,7 +457,7 @@ struct Bf16Body {
     }
     if (kPacked)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = 0; i < KD / 8; ++i) {
         o[i][0] += o[i][2];
         o[i][1] += o[i][3];
       }
@@ -463,7 +472,11 @@ struct Bf16Body {
         const float f = sink.factor(l[n]);
         auto* to = sink.at(row(n)) + 2 * (lane % 4);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) sink.store(to + i * 8, f, o[i][2 * n], o[i][2 * n + 1]);
+        for (int i = 0; i < D / 8; ++i) {
+          constexpr int kNext = PAIR ? D / 8 : 0;  // to the second KV head's sums
+          sink.store(to + i * 8, f, second[n] ? o[i + kNext][2 * n] : o[i][2 * n],
+                     second[n] ? o[i + kNext][2 * n + 1] : o[i][2 * n + 1]);
+        }
       }
   }
 };
@@ -1148,12 +1161,31 @@ mf_status check(const mf_kv_cache* cache, const mf_paged_attn_desc* a) {
   return MF_OK;
 }
 
-// Query heads of one KV head are taken together, up to what a warp's registers
-// hold (16 for bf16, 8 for float32); more are cut into even groups, each of
-// which reads the keys again.
-int head_groups(const mf_kv_cache& c, int Hq) {
+// What a row is.  Query heads of one KV head are taken together, up to what a
+// warp's registers hold (16 for bf16, 8 for float32); more are cut into even
+// groups, each of which reads the keys again.
+//
+// Where a key is 128 bytes (bf16, d 64), two KV heads make a row if the query
+// heads of both have room in it, for HBM is slow to bring pieces of 128 bytes:
+// 64 sequences of 3 K to 8 K tokens, 32 heads over 8, 111 us, 141 with a head a
+// row.  Tables with room for few units keep a head a row, which is more rows to
+// share out (one sequence of 1000 tokens 9.0 us, 9.9 in pairs; 16 of up to 1000,
+// with room for 54 a block, 12.1 and 12.2; 30 of them 18.4 and 17.4).
+constexpr int kPairs = 40;  // units a block
+
+struct Rows {
+  bool pair;
+  int Hkv, G;      // as if two KV heads were one
+  int groups, gh;  // groups of query heads per KV head, heads of a group
+};
+
+Rows rows_of(const mf_kv_cache& c, int Hq) {
   const int G = Hq / c.Hkv, most = c.dt == MF_BF16 ? 16 : 8;
-  return (G + most - 1) / most;
+  const int64_t room = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) * c.nseq * c.Hkv;
+  if (c.dt == MF_BF16 && c.d == 64 && c.Hkv % 2 == 0 && 2 * G <= most && room >= kCtas * kPairs)
+    return Rows{true, c.Hkv / 2, 2 * G, 1, 2 * G};
+  const int groups = (G + most - 1) / most;
+  return Rows{false, c.Hkv, G, groups, (G + groups - 1) / groups};
 }
 
 // Where the table has room for few places a block, blocks take whole rows:
@@ -1162,30 +1194,33 @@ int head_groups(const mf_kv_cache& c, int Hq) {
 // with in that time (14 sequences of up to 215 tokens, 8 heads a KV head: 11.1
 // us with the second launch, 9.0 without; float32, 19 of up to 491 tokens, 2
 // heads a KV head: 10.2 with, 15.1 without).
-bool whole_rows(const mf_kv_cache& c, int groups) {
+bool whole_rows(const mf_kv_cache& c, const Rows& of) {
   const int64_t few = kWarps * (c.dt == MF_BF16 ? 4 : 2);  // so rows are few, too
   const int64_t places = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit) + kRowCost;
-  const int64_t rows = int64_t(c.nseq) * c.Hkv * groups;
+  const int64_t rows = int64_t(c.nseq) * of.Hkv * of.groups;
   return places <= few && (rows + kCtas - 1) / kCtas * places <= few;
 }
 
 // Blocks past the first kCtas, where the table has room for a large line.
-int extra_blocks(const mf_kv_cache& c, int groups) {
+int extra_blocks(const mf_kv_cache& c, const Rows& of) {
   const int64_t units = int64_t(c.max_pages_per_seq) * (c.page_size / kUnit);
-  return units * c.nseq * c.Hkv * groups >= int64_t(kCtas) * kLarge ? kExtra : 0;
+  return units * c.nseq * of.Hkv * of.groups >= int64_t(kCtas) * kLarge ? kExtra : 0;
 }
 
 size_t layout(const mf_kv_cache& c, int Hq, void* ws, Params* p) {
-  const int groups = head_groups(c, Hq), G = Hq / c.Hkv, gh = (G + groups - 1) / groups;
-  const int extra = extra_blocks(c, groups), blocks = kCtas + extra;
+  const Rows of = rows_of(c, Hq);
+  const int gh = of.gh, extra = extra_blocks(c, of), blocks = kCtas + extra;
   Carve k(ws);
   float* part_o = k.take<float>(size_t(2 * blocks) * gh * c.d);
   float2* part_ml = k.take<float2>(size_t(2 * blocks) * gh);
   Shared* shared = k.take<Shared>(blocks);
   if (p) {
-    p->groups = groups;
+    p->pair = of.pair;
+    p->Hkv = of.Hkv;
+    p->G = of.G;
+    p->groups = of.groups;
     p->gh = gh;
-    p->by_rows = whole_rows(c, groups);
+    p->by_rows = whole_rows(c, of);
     p->extra = extra;
     p->part_o = part_o;
     p->part_ml = part_ml;
@@ -1233,6 +1268,10 @@ template <int D>
 cudaError_t launch_d(const Params& p, mf_dtype dt, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   if (dt == MF_BF16) {
+    if constexpr (D == 64)
+      if (p.pair)
+        return p.gh <= 8 ? launch<Bf16Body<D, 8, true>>(p, tk, tv, st)
+                         : launch<Bf16Body<D, 16, true>>(p, tk, tv, st);
     if (p.gh <= 4) return launch<Bf16Body<D, 4>>(p, tk, tv, st);
     if (p.gh <= 8) return launch<Bf16Body<D, 8>>(p, tk, tv, st);
     return launch<Bf16Body<D, 16>>(p, tk, tv, st);
@@ -1282,8 +1321,6 @@ mf_status mf_paged_attn(const mf_kv_cache* cache, const mf_paged_attn_desc* attn
   p.npages = c.npages;
   p.nseq = c.nseq;
   p.Hq = a.Hq;
-  p.Hkv = c.Hkv;
-  p.G = a.Hq / c.Hkv;
   p.page_size = c.page_size;
   p.max_pages = c.max_pages_per_seq;
   p.len_add = a.len_add;
@@ -1299,12 +1336,13 @@ mf_status mf_paged_attn(const mf_kv_cache* cache, const mf_paged_attn_desc* attn
   // of one head.  Without pages nothing is copied.
   CUtensorMap tk = {}, tv = {};
   if (c.npages > 0) {
-    const uint64_t row = uint64_t(c.d) * elem;
-    const uint64_t dims[4] = {64, uint64_t(c.npages) * c.page_size, row / 128, uint64_t(c.Hkv)};
-    const uint64_t strides[3] = {c.Hkv * row, 128, row};
+    const uint64_t row = uint64_t(c.d) * elem * (p.pair ? 2 : 1);
+    const uint64_t dims[4] = {64, uint64_t(c.npages) * c.page_size, row / 128, uint64_t(p.Hkv)};
+    const uint64_t strides[3] = {p.Hkv * row, 128, row};
     const uint32_t box[4] = {64, kUnit, uint32_t(row / 128), 1};
-    if (make_tmap_bf16(&tk, c.K, 4, dims, strides, box, 128) != cudaSuccess ||
-        make_tmap_bf16(&tv, c.V, 4, dims, strides, box, 128) != cudaSuccess)
+    const int l2 = row < 256 ? 128 : 256;
+    if (make_tmap_bf16(&tk, c.K, 4, dims, strides, box, 128, l2) != cudaSuccess ||
+        make_tmap_bf16(&tv, c.V, 4, dims, strides, box, 128, l2) != cudaSuccess)
       return fail(MF_ERR_CUDA, "paged attention: no tensor map of the page pools");
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -672,7 +672,8 @@ cudaError_t make_tmap_2d_bf16(CUtensorMap* m, const void* base, uint64_t rows, u
 }
 
 cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                           const uint64_t* strides_bytes, const uint32_t* box, int swizzle_bytes) {
+                           const uint64_t* strides_bytes, const uint32_t* box, int swizzle_bytes,
+                           int l2_bytes) {
   qk::EncodeTiled enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   cuuint64_t d[5], st[4];
@@ -689,7 +690,9 @@ cudaError_t make_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uin
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void*>(base),
                    d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   l2_bytes == 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                   : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -68,7 +68,7 @@ def test_totals_around_the_numbers_of_blocks_and_warps(dt, total):
         check_attention(c, lengths, Q, O, lse, 64 ** -0.5)
 
 
-@pytest.mark.parametrize("dt,Hq,Hkv,d,rows", [(BF, 16, 8, 64, 8), (BF, 64, 2, 128, 4),
+@pytest.mark.parametrize("dt,Hq,Hkv,d,rows", [(BF, 16, 8, 64, 4), (BF, 64, 2, 128, 4),
                                               (F32, 33, 1, 128, 5), (F32, 8, 8, 64, 8)])
 @pytest.mark.parametrize("few", [False, True], ids=["spread", "few_long"])
 def test_lines_long_enough_for_more_blocks(dt, Hq, Hkv, d, rows, few):
@@ -89,6 +89,37 @@ def test_lines_long_enough_for_more_blocks(dt, Hq, Hkv, d, rows, few):
     O, lse = mfb.paged_attn(c, Q, i32(lengths))
     mfb.sync_status()
     check_attention(c, lengths, Q, O, lse, d ** -0.5)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 8), (8, 2), (16, 4), (20, 4), (32, 4), (36, 4),
+                                    (9, 3), (15, 3), (48, 3)])
+def test_heads_of_64_dims(Hq, Hkv):
+    """Even and odd numbers of KV heads of 128 bytes a key, up to 16 query heads for two of them
+    and more, narrow tables and wide ones (two KV heads at a time); NaN and infinities among the
+    keys and values of one head stay in its own outputs."""
+    lengths = [700, 1, 0, 16, 333, 2048, 47]
+    c = filled_cache(lengths, 32, Hkv, 64, BF, 62)
+    Q = randn((len(lengths), Hq, 64), BF, 63)
+    for table in (c.page_table, widened(c, 900).page_table):
+        O, lse = mfb.paged_attn(mfb.KVCache(c.K, c.V, table), Q, i32(lengths), window=500,
+                                band_bias=-0.75, band_width=18)
+        mfb.sync_status()
+        check_attention(c, lengths, Q, O, lse, 0.125, -0.75, 18, 500)
+        G = Hq // Hkv
+        for bad in range(Hkv):
+            k = mfb.KVCache(c.K.clone(), c.V.clone(), table)
+            kh, vh = k.K.view(-1, Hkv, 64)[:, bad], k.V.view(-1, Hkv, 64)[:, bad]
+            kh[:, 3], kh[::5, 7], vh[:, 5], vh[::3, 11] = math.nan, math.inf, -math.inf, math.nan
+            O2, lse2 = mfb.paged_attn(k, Q, i32(lengths), window=500, band_bias=-0.75,
+                                      band_width=18)
+            mfb.sync_status()
+            for h in range(Hkv):
+                hs = slice(h * G, (h + 1) * G)
+                if h == bad:
+                    live = [s for s, n in enumerate(lengths) if n > 0]
+                    assert O2[live][:, hs].isnan().all() and lse2[hs][:, live].isnan().all()
+                else:
+                    assert torch.equal(O2[:, hs], O[:, hs]) and torch.equal(lse2[hs], lse[hs])
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
