@@ -274,7 +274,7 @@ struct Join {
 // pipe is enough (up to 48 and a third with 16 heads); operands and sums stay in
 // one warp's registers and no warp waits for another.  The same work as
 // tcgen05 products of 128 keys x heads, with P through shared memory and sums
-// in TMEM, took 237 us where this takes 226, and 48 where this takes 17 (short
+// in TMEM, took 237 us where this took 226 then, and 48 where 17 (short
 // rows): each tile is a chain of five hand-offs, and a row's end another two.
 //
 // A unit takes a warp 1800 cycles at 4 heads a group: 350 S, 320 weights, 220
