@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && p.npages > 0) {
     tma_prefetch_desc(&tk);
     tma_prefetch_desc(&tv);
   }

@@ -107,13 +107,14 @@ __global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks) k_rotary(const 
 
   if (threadIdx.x < live) {
     const int64_t t = t0 + threadIdx.x;
-    const int s = p.cu ? upper_index(p.cu, p.nseq, t) : int(t);
-    const int32_t first = p.start ? p.start[s] : 0;
+    const int s = p.cu ? upper_index(p.cu, p.nseq + 1, t) : int(t);
+    const bool padding = s == p.nseq;  // behind the last sequence
+    const int32_t first = p.start && !padding ? p.start[s] : 0;
     const int64_t pos = int64_t(first) + (p.cu ? t - p.cu[s] : 0);
     int64_t row = t;  // of K's and V's outputs; -1: nothing is written
-    if (p.paged) {
+    if (padding || p.paged) {
       row = -1;
-      if (first >= 0) {  // else a padding sequence
+      if (!padding && first >= 0) {  // else a padding sequence
         int32_t at = -1;
         if (pos >= 0 && pos < int64_t(p.max_pages) * p.page_size)
           at = p.page_table[int64_t(s) * p.max_pages + int(pos) / p.page_size];
@@ -251,6 +252,8 @@ mf_status check_batch(const mf_token_batch* b) {
   if (b->ntok < 0 || b->nseq < 0 || (b->nseq == 0 && b->ntok > 0))
     return fail(MF_ERR_INVALID_ARG, "negative token or sequence count, or tokens without sequences");
   if (b->ntok > INT32_MAX) return fail(MF_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens");
+  if (b->cu_seqlens && b->nseq == INT32_MAX)
+    return fail(MF_ERR_UNSUPPORTED, "more than 2^31 - 2 sequences");
   if (!b->cu_seqlens && b->ntok != b->nseq)
     return fail(MF_ERR_INVALID_ARG, "without cu_seqlens every sequence has one token");
   return MF_OK;

@@ -180,12 +180,14 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   EXPECT(!Qo || rows(*Qo, ntok, Hq, d, type, &qos));
   EXPECT(Hq <= INT32_MAX && Hk <= INT32_MAX && d <= INT32_MAX);
+  const int backward = PyObject_IsTrue(a[8]);
+  if (backward < 0) return nullptr;
   const at::Tensor q = output(Qo, *Q), k = K ? output(Ko, *K) : at::Tensor();
   const mf_status st =
       p_rope(static_cast<const mf_rope_desc*>(address(a[0])), &b, int32_t(d), dt, int32_t(Hq),
              Q->const_data_ptr(), qs, q.mutable_data_ptr(), Qo ? qos : Hq * d, int32_t(Hk),
              K ? K->const_data_ptr() : nullptr, ks, K ? k.mutable_data_ptr() : nullptr,
-             Ko ? kos : Hk * d, PyObject_IsTrue(a[8]), stream(dev));
+             Ko ? kos : Hk * d, backward, stream(dev));
   if (st != MF_OK) return PyLong_FromLong(st);
   PyObject* oq = wrapped(q, a[6]);
   if (!K) return oq;

@@ -557,8 +557,8 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     """Rotates Q [ntok, Hq, d] and, if given, K [ntok, Hk, d]: Q_out, or (Q_out, K_out).
 
     Token t of sequence s (cu_seqlens [nseq + 1], int32 on the device) has position
-    start[s] + t - cu_seqlens[s]; without cu_seqlens, start [ntok] holds every token's
-    own position.  backward=True takes gradients of the outputs to those of the inputs.
+    start[s] + t - cu_seqlens[s], and the rows of tokens past cu_seqlens[nseq] are left as
+    they were; without cu_seqlens, start [ntok] holds every token's own position.  backward=True takes gradients of the outputs to those of the inputs.
     Q_out may be Q, and K_out may be K."""
     f = _fast or _load_fast()
     r = f.rope(rp._addr, rp.phases, Q, K, start, cu_seqlens, Q_out, K_out, backward)
@@ -592,8 +592,8 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
 
 class KVCache:
     """A receiver's paged keys and values: pools [npages, page_size, Hkv, d] and the page
-    table int32 [nseq, max_pages_per_seq], all owned by the caller.  `V` with `page_table`
-    is what mapped_av reads."""
+    table int32 [nseq, max_pages_per_seq], all owned by the caller, who may change what
+    they hold but not where they lie.  `V` with `page_table` is what mapped_av reads."""
 
     def __init__(self, K, V, page_table):
         r = (_fast or _load_fast()).kv_cache(K, V, page_table)
@@ -629,7 +629,8 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     their pages, behind the lens[s] tokens (int32 on the device; None: 0) that sequence s
     holds; rotates the same tokens' queries Q [ntok, Hq, d] and returns them (None
     without Q).  cu_seqlens [nseq + 1]: the new tokens of every sequence; None: one each.
-    A negative length marks a padding sequence, whose rows are left as they were.
+    The rows of a padding sequence, marked by a negative length, and of tokens past
+    cu_seqlens[nseq] are left as they were.
     `lens` itself is not changed."""
     f = _fast or _load_fast()
     r = f.kv_append(cache._addr, cache._device, K, V, lens, None if rope is None else rope._addr,

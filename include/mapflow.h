@@ -383,7 +383,10 @@ mf_status mf_rope_phases(const double* inv_freq, int32_t n, uint64_t* phases);
 
 /* The tokens of a call: ntok packed tokens of nseq sequences.
  *  cu_seqlens: device [nseq+1], prefix sums of the tokens per sequence in this
- *              call, from 0 to ntok; NULL: one token per sequence (ntok = nseq).
+ *              call, from 0 to ntok or less; NULL: one token per sequence (ntok =
+ *              nseq).  Tokens past cu_seqlens[nseq] are padding (of a captured
+ *              call's fixed batch): their rows of every output are left as they
+ *              were.
  *  start:      device [nseq], the position of each sequence's first token in
  *              this call; NULL: 0.
  * Token t of sequence s has position start[s] + t - cu_seqlens[s].  With

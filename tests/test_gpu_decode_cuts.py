@@ -364,3 +364,70 @@ def test_append_padding_sequences_between_prompts():
     keep = torch.ones(npages * 16, dtype=torch.bool, device="cuda")
     keep[at] = False
     assert torch.equal(c.K.view(-1, 2, 64)[keep], K0.view(-1, 2, 64)[keep])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_tokens_behind_the_last_sequence(dt):
+    """A captured append and rotation of a fixed batch whose sequences fill it less and less: the
+    pools' other rows and the padding's rows of every output stay as they were."""
+    ntok, nseq, Hq, Hkv, d = 40, 3, 4, 2, 128
+    table, npages = pages([64] * nseq, 16, 86)
+    c = mfb.KVCache(randn((npages, 16, Hkv, d), dt, 87), randn((npages, 16, Hkv, d), dt, 88), table)
+    K0, V0 = c.K.clone(), c.V.clone()
+    Q, K, V = (randn((ntok, h, d), dt, 89 + i) for i, h in enumerate((Hq, Hkv, Hkv)))
+    f = mfb.rope_freqs(d)
+    rp = mfb.Rope.from_freqs(f)
+    past, cu = i32([3, 0, 20]), i32([0, 15, 15, 40])
+    Qa, Qr, Kr = (torch.zeros((ntok, h, d), dtype=dt, device="cuda") for h in (Hq, Hq, Hkv))
+
+    def run():
+        mfb.kv_append(c, K, V, past, rope=rp, Q=Q, Q_out=Qa, cu_seqlens=cu)
+        mfb.rope(rp, Q, K, start=past, cu_seqlens=cu, Q_out=Qr, K_out=Kr, backward=True)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for bounds in ([0, 15, 15, 40], [0, 15, 15, 39], [0, 7, 19, 20], [0, 0, 1, 1], [0, 0, 0, 0]):
+        cu.copy_(i32(bounds))
+        c.K.copy_(K0)
+        c.V.copy_(V0)
+        for x in (Qa, Qr, Kr):
+            x.fill_(9.0)
+        graph.replay()
+        mfb.sync_status()
+        n = bounds[-1]
+        pos = torch.cat([torch.arange(p, p + b - a)
+                         for p, a, b in zip((3, 0, 20), bounds, bounds[1:])])
+        near_rotated(Qa[:n], Q[:n], pos, f, d, False)
+        near_rotated(Qr[:n], Q[:n], pos, f, d, False, backward=True)
+        near_rotated(Kr[:n], K[:n], pos, f, d, False, backward=True)
+        for x in (Qa, Qr, Kr):
+            assert (x[n:] == 9.0).all()
+        at = torch.cat([slots(table, 16, s, p, p + b - a) for s, (p, a, b) in
+                        enumerate(zip((3, 0, 20), bounds, bounds[1:]))])
+        near_rotated(c.K.view(-1, Hkv, d)[at], K[:n], pos, f, d, False)
+        assert torch.equal(c.V.view(-1, Hkv, d)[at], V[:n])
+        keep = torch.ones(npages * 16, dtype=torch.bool, device="cuda")
+        keep[at] = False
+        for x, x0 in ((c.K, K0), (c.V, V0)):
+            assert torch.equal(x.view(-1, Hkv, d)[keep], x0.view(-1, Hkv, d)[keep])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_a_pool_without_pages(dt):
+    """No pages: sequences without tokens are empty rows, others have no key and are reported."""
+    c = mfb.KVCache.make(0, 16, 2, 64, dt, torch.full((3, 4), -1, dtype=torch.int32, device="cuda"))
+    Q = randn((3, 4, 64), dt, 92)
+    O, lse = mfb.paged_attn(c, Q, i32([0, 0, 0]))
+    mfb.sync_status()
+    assert (O == 0).all() and (lse == -math.inf).all()
+    O, lse = mfb.paged_attn(c, Q, i32([0, 30, 0]))
+    with pytest.raises(mfb.MapflowError):
+        mfb.sync_status()
+    assert (O == 0).all() and (lse == -math.inf).all()
+    mfb.sync_status()  # reported once
