@@ -522,10 +522,18 @@ class Rope:
     def __init__(self, phases, interleaved=False, scale=1.0):
         _require(phases.dtype == torch.int64 and phases.dim() == 1 and phases.is_contiguous(),
                  "phases must be a contiguous int64 tensor [rot_dim / 2]")
-        self.phases, self.interleaved, self.scale = phases, bool(interleaved), float(scale)
+        self._args = phases, bool(interleaved), float(scale)
         self._desc = RopeDesc(2 * phases.shape[0], int(self.interleaved), phases.data_ptr(),
                               self.scale)
         self._addr = C.addressof(self._desc)
+
+    # what _desc was made of: not to be set, and a copy makes its own
+    phases = property(lambda self: self._args[0])
+    interleaved = property(lambda self: self._args[1])
+    scale = property(lambda self: self._args[2])
+
+    def __reduce__(self):
+        return type(self), self._args
 
     @classmethod
     def from_freqs(cls, inv_freq, interleaved=False, scale=1.0, device="cuda"):
@@ -561,7 +569,7 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     they were; without cu_seqlens, start [ntok] holds every token's own position.  backward=True takes gradients of the outputs to those of the inputs.
     Q_out may be Q, and K_out may be K."""
     f = _fast or _load_fast()
-    r = f.rope(rp._addr, rp.phases, Q, K, start, cu_seqlens, Q_out, K_out, backward)
+    r = f.rope(rp._addr, rp._args[0], Q, K, start, cu_seqlens, Q_out, K_out, backward)
     if r is not None:
         return _made(r)
     _require(start is not None or cu_seqlens is not None, "start or cu_seqlens must be given")
@@ -608,9 +616,17 @@ class KVCache:
                         "[nseq, max_pages_per_seq]")
             _dtype_code(K.dtype)
             _refuse("a size of the pools or of the page table is past 32 bits")
-        self.K, self.V, self.page_table = K, V, page_table
+        self._args = K, V, page_table
         (self.npages, self.page_size, self.Hkv, self.d, self.nseq, self.max_pages,
          self._device, self._bytes, self._addr) = r
+
+    # what _bytes was made of: not to be set, and a copy makes its own
+    K = property(lambda self: self._args[0])
+    V = property(lambda self: self._args[1])
+    page_table = property(lambda self: self._args[2])
+
+    def __reduce__(self):
+        return type(self), self._args
 
     @property
     def _desc(self):
@@ -634,7 +650,7 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     `lens` itself is not changed."""
     f = _fast or _load_fast()
     r = f.kv_append(cache._addr, cache._device, K, V, lens, None if rope is None else rope._addr,
-                    None if rope is None else rope.phases, Q, Q_out, cu_seqlens)
+                    None if rope is None else rope._args[0], Q, Q_out, cu_seqlens)
     if r is not None:
         return None if r is True else _made(r)
     _require(K.dim() == 3, "K must be [ntok, Hkv, d]")

@@ -1,7 +1,9 @@
 """Rotary frequencies and phases, and the refusals of the receiver's decode calls
 (mf_rope, mf_kv_append, mf_paged_attn): host only, nothing here launches a kernel."""
+import copy
 import ctypes as C
 import math
+import pickle
 from fractions import Fraction
 
 import numpy as np
@@ -242,3 +244,24 @@ def test_binding_refuses_wrong_tensors(lib):
     refused(mfb.paged_attn, c, Q[:2], lens[:1])
     refused(mfb.paged_attn, c, Q[:2], lens, lse=torch.zeros(2, 4))
     refused(mfb.paged_attn, c, Q[:2], lens)                   # not on a GPU
+
+
+def test_copies_describe_their_own_tensors(lib):
+    """A deep copy or an unpickled one is of its own pools and phases; the tensors a description
+    was made of cannot be exchanged behind it."""
+    c = mfb.KVCache.make(5, 16, 2, 64, torch.float32, torch.arange(6, dtype=torch.int32).view(2, 3))
+    c.K.fill_(1.0)
+    rp = mfb.Rope.make(64, interleaved=True, scale=0.5, device="cpu")
+    for again in (copy.deepcopy, lambda x: pickle.loads(pickle.dumps(x))):
+        k = again(c)
+        d = k._desc
+        assert (d.K, d.V, d.page_table) == tuple(x.data_ptr() for x in (k.K, k.V, k.page_table))
+        assert d.K != c.K.data_ptr() and torch.equal(k.K, c.K) and d.npages == 5
+        assert torch.equal(k.page_table, c.page_table)
+        r = again(rp)
+        assert r._desc.phases == r.phases.data_ptr() != rp.phases.data_ptr()
+        assert torch.equal(r.phases, rp.phases) and r.interleaved and r.scale == 0.5
+    assert copy.copy(c)._desc.K == c.K.data_ptr()
+    for x, name in ((c, "K"), (c, "V"), (c, "page_table"), (rp, "phases"), (rp, "scale")):
+        with pytest.raises(AttributeError):
+            setattr(x, name, getattr(x, name))
