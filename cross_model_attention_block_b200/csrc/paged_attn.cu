@@ -831,6 +831,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const Cuts cuts = cuts_of(p, plan.before[kThreads]);
+  if (blockIdx.x >= kCtas && cuts.head == cuts.total) {  // a wide table's short lengths
+    if (threadIdx.x == 0) p.shared[blockIdx.x] = Shared{0, 0, 0, -1};
+    return;
+  }
   int64_t c0, c1;  // the block's run
   if (p.by_rows) {
     const int rows = p.nseq * p.Hkv * p.groups;  // few: 32 bits
@@ -1034,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   // sequences without keys
-  for (int s = blockIdx.x; s < p.nseq; s += gridDim.x) {
+  for (int s = blockIdx.x; s < p.nseq && blockIdx.x < kCtas; s += kCtas) {
     if (span_of(p, s).n > 0) continue;
     for (int i = threadIdx.x; i < p.Hq * (D / 2); i += kThreads)
       store2(static_cast<T*>(p.O) + s * p.o_stride + 2 * i, 0.f, 0.f);
