@@ -51,7 +51,9 @@ constexpr int kWarps = 8;      // of the main kernel's blocks
 // blocks.  Measured, 64 sequences of 1 K to 16 K tokens: 215 us with 8, 219 with
 // 6 or with half as many blocks, 224 without; batches of 540 and 600 places a
 // block lose (97 -> 103 us) and break even (111 -> 112), of 1000 and 1280 gain
-// (172 -> 167, 211 -> 205).
+// (172 -> 167, 211 -> 205).  A table with room for such a line brings the blocks
+// whatever the lengths: where these are short they leave at once, for 1 us (64
+// sequences of 200 tokens 16.8 -> 17.7).
 constexpr int kExtra = 2 * kCtas;
 constexpr int kRest = 8;
 constexpr int kLarge = 800;
