@@ -60,6 +60,10 @@ struct RotaryParams {
 
 constexpr int kMaxTokens = 4;  // of a block
 
+// Rows of K's and V's outputs that do not exist.
+constexpr int64_t kNoSlot = -1;   // the token's place is outside the table or the pool
+constexpr int64_t kPadding = -2;  // no token: its query is left alone, too
+
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
   T v[N];
@@ -111,10 +115,11 @@ __global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks) k_rotary(const 
     const bool padding = s == p.nseq;  // behind the last sequence
     const int32_t first = p.start && !padding ? p.start[s] : 0;
     const int64_t pos = int64_t(first) + (p.cu ? t - p.cu[s] : 0);
-    int64_t row = t;  // of K's and V's outputs; -1: nothing is written
+    int64_t row = t;  // of K's and V's outputs
     if (padding || p.paged) {
-      row = -1;
+      row = kPadding;
       if (!padding && first >= 0) {  // else a padding sequence
+        row = kNoSlot;
         int32_t at = -1;
         if (pos >= 0 && pos < int64_t(p.max_pages) * p.page_size)
           at = p.page_table[int64_t(s) * p.max_pages + int(pos) / p.page_size];
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks) k_rotary(const 
     if (token >= live) break;
     const int item = step * 32 + threadIdx.x % 32, h = item / kUnits, u = item % kUnits;
     const int64_t t = t0 + token, row = rows[token];
-    if (h >= H || row < 0) continue;
+    if (h >= H || row == kPadding || (row == kNoSlot && h >= p.Hq)) continue;
     const T* in;
     T* out;
     if (h < p.Hq) {

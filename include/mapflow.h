@@ -440,8 +440,9 @@ typedef struct {
  *  K, V [ntok][Hkv][d], Q and Q_out [ntok][Hq][d], strides as in mf_rope;
  *  Q_out may be Q.  rope NULL: K and Q are copied unrotated.
  * A token whose page lies beyond max_pages_per_seq or whose table entry is
- * outside [0, npages) is not written and sets the device status
- * (MF_ERR_INVALID_ARG via mf_sync_status).  Two tokens must not share a slot.
+ * outside [0, npages) is not written to the pools and sets the device status
+ * (MF_ERR_INVALID_ARG via mf_sync_status); its query is rotated all the same.
+ * Two tokens must not share a slot.
  * Errors: MF_ERR_INVALID_ARG, MF_ERR_UNSUPPORTED, MF_ERR_CUDA. */
 mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
                        const mf_token_batch* batch, const void* K, int64_t k_stride,
