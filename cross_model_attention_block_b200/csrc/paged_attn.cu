@@ -251,6 +251,11 @@ __device__ __forceinline__ Walk find_place(const Params& p, const PlanSmem& sm, 
 
 // ------------------------------------------------------- joining two pieces
 
+// In place of a piece's sum of weights: its unnormalised O was never written.  A
+// sum of zero is not that: keys whose logits are all -inf weigh nothing, but zero
+// times a NaN or an infinity among their values is a NaN, wherever a row is cut.
+constexpr float kNoSums = -1.f;
+
 // The factors of two pieces with maxima a and b, relative to their maximum m.
 struct Join {
   float m, ca, cb;
@@ -725,14 +730,13 @@ struct Finished {
     if (p.lse)
       p.lse[int64_t(h0 + head) * p.nseq + s] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
-  // of the sums; 0: nothing seen
+  // of the sums; 0: no weight (the sums are zero, or NaN)
   __device__ __forceinline__ static float factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
   __device__ __forceinline__ T* at(int head) const {
     return static_cast<T*>(p.O) + s * p.o_stride + int64_t(h0 + head) * D;
   }
-  // zero where nothing is seen, whatever was summed
   __device__ __forceinline__ static void store(T* o, float f, float a, float b) {
-    store2(o, f == 0.f ? 0.f : a * f, f == 0.f ? 0.f : b * f);
+    store2(o, a * f, b * f);
   }
 };
 
@@ -927,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 0 && c1 == c0) {  // an empty block
       p.shared[blockIdx.x] = Shared{0, 0, 0, -1};
       for (int i = 0; i < 2 * p.gh; ++i)
-        p.part_ml[int64_t(2) * blockIdx.x * p.gh + i] = make_float2(-INFINITY, 0.f);
+        p.part_ml[int64_t(2) * blockIdx.x * p.gh + i] = make_float2(-INFINITY, kNoSums);
     }
   }
 
@@ -1018,7 +1022,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = t % share; h < heads; h += share) {
         Piece<D> acc;
         auto add = [&](const char* from, float2 ml) {
-          if (ml.y == 0.f) return;  // nothing seen: its sums are void
           float o[D / 32];
           const float* x = reinterpret_cast<const float*>(from) + h * D + lane * (D / 32);
 #pragma unroll
@@ -1090,7 +1093,7 @@ __device__ __forceinline__ void join_blocks(const Params& p, const Shared& row, 
         const int src = left ? __ffs(left) - 1 : 0;
         const float m = __shfl_sync(0xffffffffu, ml.x, src);
         const float l = __shfl_sync(0xffffffffu, ml.y, src);
-        if (left && l != 0.f) acc.add(m, l, o[i]);  // l = 0: an empty piece, its sums void
+        if (left && l != kNoSums) acc.add(m, l, o[i]);
         left &= left - 1;
       }
     }

@@ -461,7 +461,9 @@ mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
  *  lse [Hq][nseq] float, or NULL.
  * Softmax statistics and sums are float32; for bf16 the weights are kept to
  * 2^-17.  A NaN or an infinity among the values a query sees makes its outputs
- * of that dim NaN or infinite.  A key whose page is outside the
+ * of that dim NaN or infinite, behind a logit of -inf as well (zero times either
+ * is NaN); a query that sees logits of -inf alone gets lse = -inf and otherwise
+ * O = 0.  A key whose page is outside the
  * pool or the table counts as masked and sets the device status
  * (MF_ERR_INVALID_ARG via mf_sync_status).  Rows of the pools past a
  * sequence's end, and keys outside the window, have no influence, whatever

@@ -4,12 +4,16 @@ among keys and values, biases of the type's size, angles near a quarter turn.
 The plain 64-bit evaluations and the tolerances derived beside them are those of
 test_gpu_decode.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from cross_model_attention_block_b200 import mapflow as mfb
-from tests.test_gpu_decode import BF, F32, i32, near_rotated, pages, randn, slots
+from tests.test_gpu_decode import (BF, F32, attend64, filled_cache, i32, near_rotated, pages, randn,
+                                   slots)
+from tests.test_gpu_decode_cuts import widened
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +67,49 @@ def test_one_token_each_past_the_table():
     with pytest.raises(mfb.MapflowError):
         mfb.sync_status()
     near_rotated(q, Q, torch.tensor([32, 31]), f, 128, False)
+
+
+# ------------------------------------------------------------------ attention
+
+# head groups of every kernel variant
+LAYOUTS = [(BF, 8, 2, 128), (BF, 6, 1, 128), (BF, 24, 2, 128), (BF, 8, 2, 64), (BF, 28, 4, 64),
+           (BF, 5, 1, 64), (BF, 12, 1, 64), (F32, 6, 2, 128), (F32, 7, 1, 64), (F32, 18, 2, 64)]
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,d", LAYOUTS)
+@pytest.mark.parametrize("L,low", [(2500, 2000), (60, 41), (9000, 8991)])
+def test_values_behind_logits_of_minus_infinity(dt, Hq, Hkv, d, L, low):
+    """Keys 0 .. low-1 of a row have logits of -inf, all keys of another row: a NaN or an infinity
+    among their values is a NaN in that dim, wherever the row is cut (alone or in a batch, behind
+    a tight table or a wide one), and the other dims are those of the keys that are left."""
+    lengths, G = [L, L, 33, 700], Hq // Hkv
+    c = filled_cache(lengths, 16, Hkv, d, dt, 100)
+    kf, vf = c.K.view(-1, Hkv, d), c.V.view(-1, Hkv, d)
+    Q = randn((4, Hq, d), dt, 101)
+    Q[:, :, 0] = Q[:, :, 0].abs() + 0.5
+    at = [slots(c.page_table, 16, s, 0, n) for s, n in enumerate(lengths)]
+    kf[at[0][:low], :, 0] = -math.inf
+    kf[at[1], :, 0] = -math.inf
+    vf[at[0][low // 3], :, 5], vf[at[0][low // 2], :, 9] = math.nan, math.inf
+    vf[at[1][L // 2], :, 3], vf[at[1][0], :, 7] = math.nan, -math.inf
+    other = torch.ones(d, dtype=torch.bool, device="cuda")
+    for n in (1, 2, 4):                               # sequences in the batch
+        for table in (c.page_table, widened(c, c.max_pages + 600).page_table):
+            k = mfb.KVCache(c.K, c.V, table[:n].contiguous())
+            O, lse = mfb.paged_attn(k, Q[:n], i32(lengths[:n]))
+            mfb.sync_status()
+            other[:] = True
+            other[[5, 9]] = False
+            assert O[0][:, ~other].isnan().all()
+            for h in range(Hkv):
+                hs = slice(h * G, (h + 1) * G)
+                o, e, tol, delta = attend64(Q[0, hs].double(), kf[at[0][low:], h].double(),
+                                            vf[at[0][low:], h].double(), d ** -0.5, 0.0, 0, 0)
+                tol = tol + torch.finfo(dt).eps / 2 * o.abs()
+                assert ((O[0, hs].double() - o).abs() <= tol)[:, other].all()
+                assert ((lse[hs, 0].double() - e).abs() <= delta + 2.0 ** -22 * e.abs()).all()
+            if n > 1:
+                other[:] = True
+                other[[3, 7]] = False
+                assert O[1][:, ~other].isnan().all() and (O[1][:, other] == 0).all()
+                assert (lse[:, 1] == -math.inf).all()
