@@ -276,6 +276,12 @@ struct Join {
 // of a product free: rows 8..15 then take the remainders and the two terms
 // cost one product.
 //
+// A remainder is zero or negative as often as not, and must not meet an infinity
+// among the values, which the first terms' products already carry: sums of packed
+// remainders are dropped where those of the first terms are infinite, and the
+// unpacked remainders' products are taken with the values held to the largest
+// finite bf16 (one instruction a register, 32 a unit at 128 dims).
+//
 // Why warp-level products: a unit's 32 take 256 cycles of an SM quarter's tensor
 // pipe, and HBM brings its two warps a unit each in 2260, so a quarter of that
 // pipe is enough (up to 48 and a third with 16 heads); operands and sums stay in
@@ -310,6 +316,14 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Infinities to the largest finite bf16, with their sign.  Their products with
+// remainders stay finite unless three keys of a unit have infinities in a dim and
+// weights above 2^7 (a remainder is at most 2^-8 of its weight's power of two).
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t v) {
+  asm("min.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x7f7f7f7fu));
+  return v;
 }
 
 // HEADS: 4, 8 or 16 query heads of a row at most.  PAIR: a row has two KV heads,
@@ -448,6 +462,8 @@ struct Bf16Body {
         } else {
           mma16816(o[2 * i], hi[0][0], hi[n][0], hi[0][1], hi[n][1], v[0], v[1]);
           mma16816(o[2 * i + 1], hi[0][0], hi[n][0], hi[0][1], hi[n][1], v[2], v[3]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = finite_bf16(v[k]);
           mma16816(o[2 * i], lo[0][0], lo[n][0], lo[0][1], lo[n][1], v[0], v[1]);
           mma16816(o[2 * i + 1], lo[0][0], lo[n][0], lo[0][1], lo[n][1], v[2], v[3]);
         }
@@ -464,10 +480,10 @@ struct Bf16Body {
     }
     if (kPacked)
 #pragma unroll
-      for (int i = 0; i < KD / 8; ++i) {
-        o[i][0] += o[i][2];
-        o[i][1] += o[i][3];
-      }
+      for (int i = 0; i < KD / 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (fabsf(o[i][c]) != INFINITY) o[i][c] += o[i][2 + c];
   }
   // Hands every row to `sink`.
   template <class Sink>

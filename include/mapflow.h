@@ -460,11 +460,12 @@ mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
  *  strides (elements between sequences) multiples of 16 bytes; O may be Q.
  *  lse [Hq][nseq] float, or NULL.
  * Softmax statistics and sums are float32; for bf16 the weights are kept to
- * 2^-17.  A NaN or an infinity among the values a query sees makes its outputs
- * of that dim NaN or infinite, behind a logit of -inf as well (zero times either
- * is NaN); a query that sees logits of -inf alone gets lse = -inf and otherwise
- * O = 0.  A key whose page is outside the
- * pool or the table counts as masked and sets the device status
+ * 2^-17.  A NaN among the values a query sees makes its output of that dim NaN,
+ * an infinity makes it that infinity, or NaN where it meets its opposite or a
+ * weight of zero (a logit of -inf, or one that lies below the row's largest by
+ * more than a float32 exponent spans, some 87).  A query that sees logits of
+ * -inf alone gets lse = -inf and O = 0, but for such NaN.  A key whose page is
+ * outside the pool or the table counts as masked and sets the device status
  * (MF_ERR_INVALID_ARG via mf_sync_status).  Rows of the pools past a
  * sequence's end, and keys outside the window, have no influence, whatever
  * they hold.  Results do not depend on scheduling.

@@ -113,3 +113,39 @@ def test_values_behind_logits_of_minus_infinity(dt, Hq, Hkv, d, L, low):
                 other[[3, 7]] = False
                 assert O[1][:, ~other].isnan().all() and (O[1][:, other] == 0).all()
                 assert (lse[:, 1] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,d", LAYOUTS)
+@pytest.mark.parametrize("lengths", [[2500, 17, 700], [60, 1], [9000]], ids=len)
+def test_infinities_among_values(dt, Hq, Hkv, d, lengths):
+    """An infinity among the values makes its dim that infinity, both signs or a NaN make it NaN,
+    in its own KV head alone; every other output keeps its bits.  Logits lie within 40 of one
+    another, so that every weight is far from a float32's smallest."""
+    n, G = len(lengths), Hq // Hkv
+    c = filled_cache(lengths, 16, Hkv, d, dt, 110)
+    Q = randn((n, Hq, d), dt, 111, 0.5)
+    wide = widened(c, c.max_pages + 600).page_table
+    plain = [mfb.paged_attn(mfb.KVCache(c.K, c.V, t), Q, i32(lengths))[0]
+             for t in (c.page_table, wide)]
+    want = [x.clone() for x in plain]
+    vf, r = c.V.view(-1, Hkv, d), np.random.default_rng(7)
+    for s, L in enumerate(lengths):
+        at = slots(c.page_table, 16, s, 0, L)
+        h, hit = s % Hkv, {}
+        for dim in range(4, d, 5):
+            j, kind = int(r.integers(L)), float(r.choice([math.inf, -math.inf, math.nan]))
+            hit.setdefault(dim, []).append(kind)
+            vf[at[j], h, dim] = kind
+        if L > 1:                                     # both signs in one dim; one in every key
+            vf[at[0], h, 1], vf[at[L - 1], h, 1] = math.inf, -math.inf
+            vf[at, h, 2] = -math.inf
+            hit[1], hit[2] = [math.nan], [-math.inf]
+        for dim, kinds in hit.items():
+            for x in want:
+                x[s, h * G:(h + 1) * G, dim] = kinds[0]
+    for t, x in zip((c.page_table, wide), want):
+        O, lse = mfb.paged_attn(mfb.KVCache(c.K, c.V, t), Q, i32(lengths))
+        mfb.sync_status()
+        assert torch.equal(O.isnan(), x.isnan())
+        assert torch.equal(O.nan_to_num(nan=0.0), x.nan_to_num(nan=0.0))
+        assert lse.isfinite().all()
