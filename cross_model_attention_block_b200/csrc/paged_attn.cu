@@ -32,6 +32,7 @@
 // the cuts, 21 at 6.4 TB/s and 6 to join; 1 K tokens 9.2 us, all of it latency.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 
@@ -66,7 +67,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Shared {  // a row that blocks v0 .. v1 share (v1 < v0: none)
-  int s, r;      // its sequence, and which of the sequence's rows
+  int s, r;      // its sequence, and which of the sequence's rows (marked)
   int v0, v1;
 };
 
@@ -83,6 +84,7 @@ struct Params {
   bool by_rows;    // blocks take whole rows
   int extra;       // blocks past the first kCtas
   float scale2, bias2;  // times log2 e
+  float bias;           // as it is: of rows that lie inside the band
   // workspace: pieces of the rows that blocks share (two per block: of the row
   // its run begins in and of the row it ends in); entry b of `shared`: the row
   // whose first block boundary is the one before block b
@@ -94,8 +96,14 @@ struct Params {
 
 // ------------------------------------------------------------------ the plan
 
+// In Span's band_lo (keys lie below 2^31 - 16): no key is in the band; every key
+// is, and its bias, which moves no weight, is left to the log-sum-exp.  A bias of
+// any size takes no digits from the logits of such rows.
+constexpr int kNoBand = INT32_MAX - 1;
+constexpr int kAllBand = INT32_MAX;
+
 struct Span {  // the keys [lo, len) of a sequence, and its units
-  int lo, len, band_lo;  // the band covers keys from band_lo on
+  int lo, len, band_lo;  // keys from band_lo on get the bias
   int first, n;          // first unit, units
 };
 
@@ -108,7 +116,8 @@ __device__ __forceinline__ Span span_of(const Params& p, int s) {
   Span k;
   k.len = int(max(int64_t(0), min(L, int64_t(p.max_pages) * p.page_size)));
   k.lo = p.window > 0 ? min(clamp_int(L - p.window), k.len) : 0;
-  k.band_lo = p.band > 0 ? clamp_int(L - p.band) : INT32_MAX;
+  k.band_lo = p.band > 0 ? min(clamp_int(L - p.band), kNoBand) : kNoBand;
+  if (k.band_lo <= k.lo) k.band_lo = kAllBand;
   k.first = k.lo / kUnit;
   k.n = k.len > k.lo ? (k.len + kUnit - 1) / kUnit - k.first : 0;
   return k;
@@ -148,6 +157,16 @@ struct Cuts {
 __device__ __forceinline__ Cuts cuts_of(const Params& p, int64_t total) {
   const bool large = p.extra > 0 && total >= int64_t(kCtas) * kLarge;
   return Cuts{total, large ? total - total / kRest : total, p.extra};
+}
+
+// Which of a sequence's rows, below 2^16, with a mark where it lies inside the
+// band: whoever ends a shared row need not look up its span.
+__device__ __forceinline__ int marked(int r, const Span& k) {
+  return k.band_lo == kAllBand ? r | 1 << 16 : r;
+}
+__device__ __forceinline__ int row_of(int mark) { return mark & 0xffff; }
+__device__ __forceinline__ float bias_of(const Params& p, int mark) {
+  return mark >> 16 ? p.bias : 0.f;
 }
 
 // A place in the line: a unit, and how much of the run is left from there.
@@ -742,9 +761,11 @@ struct Finished {
   using T = T_;
   const Params& p;
   int s, h0;
+  float bias;  // what its log-sum-exp lacks
   __device__ __forceinline__ void stats(int head, float m, float l) const {
     if (p.lse)
-      p.lse[int64_t(h0 + head) * p.nseq + s] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      p.lse[int64_t(h0 + head) * p.nseq + s] =
+          l == 0.f ? -INFINITY : fmaf(m + log2f(l), kLn2, bias);
   }
   // of the sums; 0: no weight (the sums are zero, or NaN)
   __device__ __forceinline__ static float factor(float l) { return l == 0.f ? 0.f : 1.f / l; }
@@ -938,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u0 == c0 && u1 > u0) {
       const int64_t row = u0 - at.g;  // its first unit, if that is before the block
       const bool full = cuts.total >= kCtas;  // else blocks hold a place or none
-      Shared x{at.s, at.r, 0, -1};
+      Shared x{at.s, marked(at.r, at.k), 0, -1};
       if (begun && row >= (full ? cuts.at(blockIdx.x - 1) : u0 - 1)) {
         x.v0 = full ? blockIdx.x - 1 : cuts.holder(row);
         x.v1 = cuts.holder(row + at.k.n - 1);
@@ -979,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) break;
     body.finish();
     if (whole) {
-      body.put(heads, Finished<T, D>{p, at.s, h0});
+      body.put(heads, Finished<T, D>{p, at.s, h0, at.k.band_lo == kAllBand ? p.bias : 0.f});
     } else {
       // the first row's piece keeps out of the ring, which may be in use; the
       // last's, when all is read, goes there
@@ -987,9 +1008,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* to = reinterpret_cast<float*>(begun ? smem + S::kOffPieces + warp * S::kPiece : ring);
       body.put(heads, PieceAt<D>{to, join_ml[end][warp]});
       if (begun)
-        cut.s = at.s, cut.r = at.r, cut.through = at.g + n < at.k.n;
+        cut.s = at.s, cut.r = marked(at.r, at.k), cut.through = at.g + n < at.k.n;
       else
-        cut.s_end = at.s, cut.r_end = at.r;
+        cut.s_end = at.s, cut.r_end = marked(at.r, at.k);
     }
     begun = false;
     at.g += n - 1;
@@ -1027,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int v = __ffs(rest) - 2;
       const int lead = v < 0 ? __ffs(any) - 1 : v;  // the warp of its first piece
       const Cut& of = cuts_in[lead];
-      const int s = v < 0 ? of.s : of.s_end, r = v < 0 ? of.r : of.r_end;
+      const int s = v < 0 ? of.s : of.s_end, mark = v < 0 ? of.r : of.r_end, r = row_of(mark);
       const int group = r % p.groups, heads = min(p.gh, p.G - group * p.gh);
       bool open = v >= 0 || ((through >> lead) & 1);  // goes on after the pieces so far
       uint32_t more = 0;                              // warps with its further pieces
@@ -1052,7 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           add(smem + S::kOffPieces + k * S::kPiece, join_ml[0][k][h]);
         }
         if (v >= 0 && !open)
-          put_row(Finished<T, D>{p, s, r / p.groups * p.G + group * p.gh}, h, acc);
+          put_row(Finished<T, D>{p, s, r / p.groups * p.G + group * p.gh, bias_of(p, mark)}, h, acc);
         else
           put_row(piece_at<D>(p, 2 * blockIdx.x + (v < 0 ? 0 : 1)), h, acc);
       }
@@ -1126,24 +1147,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) k_paged_join(const Params 
   // lane i: the boundary before block blockIdx.x * 8 + i
   Shared row{0, 0, 0, -1};
   if (lane < kJoinWarps && w < kCtas + p.extra) row = p.shared[w];
-  const bool split = row.v0 <= row.v1 && head < min(p.gh, p.G - row.r % p.groups * p.gh);
+  const bool split = row.v0 <= row.v1 && head < min(p.gh, p.G - row_of(row.r) % p.groups * p.gh);
   const unsigned mine = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 < kJoinAlone);
   unsigned shared = __ballot_sync(0xffffffffu, split && row.v1 - row.v0 >= kJoinAlone);
-  auto row_of = [&](int i) {
+  auto get_row = [&](int i) {
     return Shared{__shfl_sync(0xffffffffu, row.s, i), __shfl_sync(0xffffffffu, row.r, i),
                   __shfl_sync(0xffffffffu, row.v0, i), __shfl_sync(0xffffffffu, row.v1, i)};
   };
   auto finish = [&](const Shared& x, const Piece<D>& acc) {
-    put_row(Finished<T, D>{p, x.s, x.r / p.groups * p.G + x.r % p.groups * p.gh}, head, acc);
+    const int r = row_of(x.r);
+    put_row(Finished<T, D>{p, x.s, r / p.groups * p.G + r % p.groups * p.gh, bias_of(p, x.r)},
+            head, acc);
   };
   if ((mine >> warp) & 1) {
-    const Shared x = row_of(warp);
+    const Shared x = get_row(warp);
     Piece<D> acc;
     join_blocks<D>(p, x, head, 0, 1, acc);
     finish(x, acc);
   }
   while (shared) {  // the same in every warp
-    const Shared x = row_of(__ffs(shared) - 1);
+    const Shared x = get_row(__ffs(shared) - 1);
     shared &= shared - 1;
     Piece<D> acc;
     join_blocks<D>(p, x, head, warp, kJoinWarps, acc);
@@ -1183,6 +1206,9 @@ mf_status check(const mf_kv_cache* cache, const mf_paged_attn_desc* a) {
     return fail(MF_ERR_INVALID_ARG, "scale or band_bias not finite");
   if (a->band_width < 0 || a->window < 0)
     return fail(MF_ERR_INVALID_ARG, "band_width or window < 0");
+  if (!std::isfinite(a->scale * kLog2e) ||
+      (a->band_width > 0 && a->band_bias * kLog2e == INFINITY))
+    return fail(MF_ERR_INVALID_ARG, "scale or band_bias times log2 e not finite");
   return MF_OK;
 }
 
@@ -1352,7 +1378,8 @@ mf_status mf_paged_attn(const mf_kv_cache* cache, const mf_paged_attn_desc* attn
   p.band = a.band_width;
   p.window = a.window;
   p.scale2 = a.scale * kLog2e;
-  p.bias2 = a.band_bias * kLog2e;
+  p.bias = a.band_bias;
+  p.bias2 = std::fmax(a.band_bias * kLog2e, -FLT_MAX);  // the type's lowest value stays finite
   p.status = status_word();
   if (!p.status) return fail(MF_ERR_CUDA, "no CUDA device");
 

@@ -454,7 +454,10 @@ mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
  *   x_j = scale q.k_j + band_bias [L-1-j < band_width],  j < L, L-1-j < window
  *   O = sum_j softmax(x)_j v_j,  lse = log sum_j exp x_j
  * (the band of mf_attn_desc; window 0: no limit).  Query head h reads KV head
- * floor(h Hkv / Hq).
+ * floor(h Hkv / Hq).  A band_bias of the type's lowest value leaves the band's
+ * keys no weight where a query sees others; where it sees the band alone, the
+ * bias changes lse only.  scale, and a positive band_bias that has a band, must be
+ * finite times log2 e.
  *  lens: device [nseq].  A sequence with L <= 0 gets O = 0 and lse = -inf.
  *  Q [nseq][Hq][d] and O [nseq][Hq][d] of the cache's dtype, 16-byte aligned,
  *  strides (elements between sequences) multiples of 16 bytes; O may be Q.

@@ -149,3 +149,41 @@ def test_infinities_among_values(dt, Hq, Hkv, d, lengths):
         assert torch.equal(O.isnan(), x.isnan())
         assert torch.equal(O.nan_to_num(nan=0.0), x.nan_to_num(nan=0.0))
         assert lse.isfinite().all()
+
+
+LOWEST = float(torch.finfo(F32).min)
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,d", LAYOUTS[:1] + LAYOUTS[2:4] + LAYOUTS[7:9])
+@pytest.mark.parametrize("bias", [LOWEST, -1e30, -3e4, 3e4, 2.3e38])
+@pytest.mark.parametrize("window", [0, 64])
+def test_band_bias_of_any_size(dt, Hq, Hkv, d, bias, window):
+    """A row that lies inside the band, as all of a short sequence or of a short window does, has
+    the weights of a row without one and a log-sum-exp further by the bias; a bias far below the
+    logits masks the band's keys of a longer row."""
+    lengths, band, G = [1, 40, 100, 101, 300, 9000], 100, Hq // Hkv
+    c = filled_cache(lengths, 16, Hkv, d, dt, 120, window=window)
+    Q = randn((len(lengths), Hq, d), dt, 121)
+    for table in (c.page_table, widened(c, c.max_pages + 600).page_table):
+        k = mfb.KVCache(c.K, c.V, table)
+        O, lse = mfb.paged_attn(k, Q, i32(lengths), band_bias=bias, band_width=band, window=window)
+        mfb.sync_status()
+        for s, L in enumerate(lengths):
+            lo, hi, shift = max(0, L - window) if window else 0, L, bias
+            if lo < L - band:                         # longer than the band
+                if bias > 0:
+                    continue
+                hi, shift = L - band, 0.0             # logits lie within 1e3 of zero
+            at = slots(c.page_table, 16, s, lo, hi)
+            for h in range(Hkv):
+                hs = slice(h * G, (h + 1) * G)
+                o, e, tol, delta = attend64(Q[s, hs].double(),
+                                            c.K.view(-1, Hkv, d)[at, h].double(),
+                                            c.V.view(-1, Hkv, d)[at, h].double(), d ** -0.5, 0.0, 0,
+                                            0)
+                tol = tol + torch.finfo(dt).eps / 2 * o.abs()
+                assert ((O[s, hs].double() - o).abs() <= tol).all(), (s, L)
+                e = e + shift
+                # the sum with the bias rounds once more, at the bias's size
+                err = (lse[hs, s].double() - e).abs()
+                assert (err <= delta + 2.0 ** -22 * e.abs()).all(), (s, L)
