@@ -7,9 +7,10 @@
 //
 // A token's pair i turns by position * f_i.  The angle is held as 64-bit
 // fixed-point turns: position * phase_i modulo 2^64 drops whole turns without
-// rounding, so the angle is good to 2^-33 turns at any 32-bit position (a
-// float32 product is off by 0.004 rad at position 100,000).  Its top 32 bits
-// go to float32 half turns and sincospif.
+// rounding, at any 32-bit position (a float32 product is off by 0.004 rad at
+// position 100,000).  The nearest quarter turn is taken off in the integer and
+// turns cosine and sine afterwards; what is left, at most an eighth of a turn,
+// goes to sincospif as float32 half turns, good to 2^-24 of itself.
 //
 // Bound by memory: every element is read and written once, a few FMAs each.
 // A block first places its tokens (sequence, position, page) and computes
@@ -138,7 +139,18 @@ __global__ void __launch_bounds__(kRotaryThreads, kRotaryBlocks) k_rotary(const 
     if (pair >= p.half) continue;
     const uint64_t angle = uint64_t(positions[token]) * p.phases[pair];
     float si, co;
-    sincospif(float(int32_t(angle >> 32)) * 0x1p-31f, &si, &co);
+    const int quarters = int((angle + (uint64_t(1) << 61)) >> 62);
+    const int64_t rest = int64_t(angle - (uint64_t(quarters) << 62));
+    sincospif(float(rest) * 0x1p-63f, &si, &co);
+    if (quarters & 1) {
+      const float x = co;
+      co = -si;
+      si = x;
+    }
+    if (quarters & 2) {
+      co = -co;
+      si = -si;
+    }
     const int u = pair / VEC, c = pair % VEC / kIn;
     turns[token][(c * kUnits + u) * kIn + pair % kIn] =
         make_float2(co * p.scale, si * (p.backward ? -p.scale : p.scale));

@@ -69,6 +69,31 @@ def test_one_token_each_past_the_table():
     near_rotated(q, Q, torch.tensor([32, 31]), f, 128, False)
 
 
+# ------------------------------------------------------------------ angles
+
+def test_angles_near_quarter_turns():
+    """Cosines and sines near their zeros keep their digits.  An angle's distance from the nearest
+    quarter turn is rounded to float32 (2^-24 of it, or 2^-34 turns where that is more); a sine
+    of an eighth of a turn or less passes no more than that on, relative, and sincospif's 2 units
+    (2^-23 each), and the cosine of so small an angle less: 2^-21 of the value and 2^-33 pi."""
+    r, n = np.random.default_rng(11), 32
+    off = [0, 1, -1, 1 << 30, -(1 << 30)] + [
+        int(s * 2.0 ** e) for s, e in zip(r.choice([-1, 1], 123), r.uniform(28, 61, 123))]
+    angles = [(q << 62) + d for d in off for q in range(4)]
+    x = torch.zeros(1, 1, 2 * n, device="cuda")
+    x[..., :n] = 1.0                                  # a pair's outputs: its cosine and its sine
+    for k in range(0, len(angles), n):
+        part = angles[k:k + n]
+        phases = torch.from_numpy(np.array([a % 2 ** 64 for a in part], np.uint64).view(np.int64))
+        y = mfb.rope(mfb.Rope(phases.cuda()), x, start=i32([1]))[0, 0].double().cpu()
+        for i, a in enumerate(part):
+            q, d = (a + (1 << 61)) >> 62, ((a + (1 << 61)) % (1 << 62)) - (1 << 61)
+            co, si = math.cos(2 * math.pi * d / 2 ** 64), math.sin(2 * math.pi * d / 2 ** 64)
+            want = [(co, si), (-si, co), (-co, -si), (si, -co)][q % 4]
+            for got, w in zip((float(y[i]), float(y[n + i])), want):
+                assert abs(got - w) <= 2.0 ** -21 * abs(w) + 2.0 ** -33 * math.pi, (a, got, w)
+
+
 # ------------------------------------------------------------------ attention
 
 # head groups of every kernel variant
