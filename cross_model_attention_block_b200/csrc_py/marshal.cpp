@@ -6,15 +6,16 @@
 // checks, allocations and stream lookup in Python took 9 to 13 us a call, here
 // 1 to 2.
 //
-// Each function makes the call and returns its outputs, or an int, the status
-// of a call that failed, or None where an argument is not of the plain kind
-// (wrong type or shape, another device than the current one, not on a GPU):
-// mapflow.py then looks closer, and raises or makes the call itself.
+// Each function makes the call on its tensors' device, whichever is current, and
+// returns its outputs, or an int, the status of a call that failed, or None where
+// it refuses an argument (wrong type or shape, several devices, not on a GPU):
+// mapflow.py then says which, and raises.
 #include <Python.h>
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -119,6 +120,14 @@ mf_stream_t stream(int dev) {
   return reinterpret_cast<mf_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
 }
 
+// Makes `dev` current for a call, where it is not.
+struct On {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit On(int dev) {
+    if (dev != c10::cuda::current_device()) guard.set_index(c10::DeviceIndex(dev));
+  }
+};
+
 #define EXPECT(cond) \
   if (!(cond)) Py_RETURN_NONE
 
@@ -164,8 +173,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    *Ko = tensor(a[7], ok);
   EXPECT(ok && phases && Q && (start || cu) && (K || !Ko) && Q->is_cuda() && Q->dim() == 3);
   const int dev = Q->get_device();
-  EXPECT(dev == c10::cuda::current_device() && on(phases, dev) && on(K, dev) && on(start, dev) &&
-         on(cu, dev) && on(Qo, dev) && on(Ko, dev));
+  EXPECT(on(phases, dev) && on(K, dev) && on(start, dev) && on(cu, dev) && on(Qo, dev) &&
+         on(Ko, dev));
   const int64_t ntok = Q->size(0), Hq = Q->size(1), d = Q->size(2);
   const at::ScalarType type = Q->scalar_type();
   mf_dtype dt;
@@ -182,6 +191,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   EXPECT(Hq <= INT32_MAX && Hk <= INT32_MAX && d <= INT32_MAX);
   const int backward = PyObject_IsTrue(a[8]);
   if (backward < 0) return nullptr;
+  const On here(dev);
   const at::Tensor q = output(Qo, *Q), k = K ? output(Ko, *K) : at::Tensor();
   const mf_status st =
       p_rope(static_cast<const mf_rope_desc*>(address(a[0])), &b, int32_t(d), dt, int32_t(Hq),
@@ -211,8 +221,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    *phases = tensor(a[6], ok), *Q = tensor(a[7], ok), *Qo = tensor(a[8], ok),
                    *cu = tensor(a[9], ok);
   EXPECT(ok && K && V && (Q || !Qo) && dev >= 0 && K->is_cuda() && K->dim() == 3);
-  EXPECT(dev == c10::cuda::current_device() && on(K, dev) && on(V, dev) && on(lens, dev) &&
-         on(phases, dev) && on(Q, dev) && on(Qo, dev) && on(cu, dev));
+  EXPECT(on(K, dev) && on(V, dev) && on(lens, dev) && on(phases, dev) && on(Q, dev) &&
+         on(Qo, dev) && on(cu, dev));
   const at::ScalarType type = c->dt == MF_BF16 ? at::kBFloat16 : at::kFloat;
   const int64_t ntok = K->size(0), d = c->d;
   mf_token_batch b;
@@ -225,6 +235,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     EXPECT(rows(*Q, ntok, Hq, d, type, &qs));
     EXPECT(!Qo || rows(*Qo, ntok, Hq, d, type, &qos));
   }
+  const On here(dev);
   const at::Tensor q = Q ? output(Qo, *Q) : at::Tensor();
   const mf_status st =
       p_append(c, static_cast<const mf_rope_desc*>(address(a[5])), &b, K->const_data_ptr(), ks,
@@ -247,8 +258,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *Q = tensor(a[2], ok), *lens = tensor(a[3], ok), *O = tensor(a[4], ok),
                    *lse = tensor(a[5], ok), *ws = tensor(a[6], ok);
   EXPECT(ok && Q && lens && dev >= 0 && Q->is_cuda() && Q->dim() == 3);
-  EXPECT(dev == c10::cuda::current_device() && on(Q, dev) && on(lens, dev) && on(O, dev) &&
-         on(lse, dev) && on(ws, dev));
+  EXPECT(on(Q, dev) && on(lens, dev) && on(O, dev) && on(lse, dev) && on(ws, dev));
   const at::ScalarType type = c->dt == MF_BF16 ? at::kBFloat16 : at::kFloat;
   const int64_t nseq = c->nseq, d = c->d, Hq = Q->size(1);
   int64_t qs = 0, os = 0;
@@ -261,6 +271,7 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   EXPECT(number(a[7], &desc.len_add) && number(a[8], &desc.scale) &&
          number(a[9], &desc.band_bias) && number(a[10], &desc.band_width) &&
          number(a[11], &desc.window));
+  const On here(dev);
   const size_t bytes = p_attn_ws(c, &desc);
   EXPECT(bytes > 0);
   at::Tensor own;

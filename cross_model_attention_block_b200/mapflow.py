@@ -444,9 +444,9 @@ def _require(ok, msg):
         _refuse(msg)
 
 
-# The decode calls go through _fast, which checks its arguments, makes the call and
-# returns None where one is not of the plain kind; the checks below then say what is
-# wrong, or the call is made from here (on another device than the current one).
+# The decode calls are made by _fast (csrc_py/marshal.cpp), which checks its arguments,
+# makes the call on their device and returns None where it refuses one; the checks
+# below then say what is wrong, and make no call.
 
 def _load_fast():
     global _fast
@@ -470,15 +470,14 @@ def _made(r):
 
 
 def _rows(name, t, ntok, H, d, dtype):
-    """Checks a [ntok, H, d] tensor whose heads are d apart; elements between tokens."""
+    """Checks a [ntok, H, d] tensor whose heads are d apart."""
     if t.shape != (ntok, H, d):
         _refuse(f"{name} must be [{ntok}, {H}, {d}], got {tuple(t.shape)}")
     if t.dtype != dtype:
         _refuse(f"{name} must be {dtype}, got {t.dtype}")
-    token, head, dim = t.stride()
+    _, head, dim = t.stride()
     if dim != 1 or (head != d and H != 1):
         _refuse(f"{name}'s heads must be {d} elements apart")
-    return token if ntok > 1 else H * d
 
 
 def _index(name, t, n):
@@ -486,22 +485,12 @@ def _index(name, t, n):
         _refuse(f"{name} must be a contiguous int32 tensor of {n} entries")
 
 
-def _new_like(t):
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
-def _call(device, tensors, f, *args):
-    """f(*args, stream) on the current stream of the tensors' device (its index)."""
-    for t in tensors:
-        if t is not None and t.get_device() != device or device < 0:
-            _refuse("every tensor must be on one CUDA device")
-    # the raw handles: torch.cuda's objects around them cost as much as a launch
-    stream = torch._C._cuda_getCurrentRawStream(device)
-    if torch._C._cuda_getDevice() == device:
-        _check(f(*args, stream))
-    else:
-        with torch.cuda.device(device):
-            _check(f(*args, stream))
+def _refuse_the_rest(*tensors):
+    """The last refusals of a call: tensors apart, or arguments that are none."""
+    given = [t for t in tensors if t is not None]
+    if any(not t.is_cuda or t.device != given[0].device for t in given):
+        _refuse("every tensor must be on one CUDA device")
+    _refuse("an argument is not of a kind that the call takes")
 
 
 def rope_freqs(rot_dim, base=10000.0, scaling="none", factor=1.0, original_length=0.0, low=1.0,
@@ -551,13 +540,12 @@ class Rope:
 
 
 def _batch(ntok, start, cu_seqlens):
-    nseq = ntok if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    nseq = ntok
     if cu_seqlens is not None:
+        nseq = max(cu_seqlens.numel(), 1) - 1
         _index("cu_seqlens", cu_seqlens, nseq + 1)
     if start is not None:
         _index("start", start, nseq)
-    return TokenBatch(ntok, nseq, None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                      None if start is None else start.data_ptr())
 
 
 def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=None,
@@ -566,7 +554,8 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
 
     Token t of sequence s (cu_seqlens [nseq + 1], int32 on the device) has position
     start[s] + t - cu_seqlens[s], and the rows of tokens past cu_seqlens[nseq] are left as
-    they were; without cu_seqlens, start [ntok] holds every token's own position.  backward=True takes gradients of the outputs to those of the inputs.
+    they were; without cu_seqlens, start [ntok] holds every token's own position.
+    backward=True takes gradients of the outputs to those of the inputs.
     Q_out may be Q, and K_out may be K."""
     f = _fast or _load_fast()
     r = f.rope(rp._addr, rp._args[0], Q, K, start, cu_seqlens, Q_out, K_out, backward)
@@ -575,27 +564,19 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     _require(start is not None or cu_seqlens is not None, "start or cu_seqlens must be given")
     _require(Q.dim() == 3, "Q must be [ntok, Hq, d]")
     ntok, Hq, d = Q.shape
-    dt = Q.dtype
-    b = _batch(ntok, start, cu_seqlens)
-    qs = _rows("Q", Q, ntok, Hq, d, dt)
-    if Q_out is None:
-        Q_out = _new_like(Q)
-    qos = _rows("Q_out", Q_out, ntok, Hq, d, dt)
-    kargs = (0, None, 0, None, 0)
+    _dtype_code(Q.dtype)
+    _batch(ntok, start, cu_seqlens)
+    for name, t in (("Q", Q), ("Q_out", Q_out)):
+        if t is not None:
+            _rows(name, t, ntok, Hq, d, Q.dtype)
     if K is not None:
         _require(K.dim() == 3 and K.shape[1] > 0, "K must be [ntok, Hk, d]")
-        Hk = K.shape[1]
-        ks = _rows("K", K, ntok, Hk, d, dt)
-        if K_out is None:
-            K_out = _new_like(K)
-        kos = _rows("K_out", K_out, ntok, Hk, d, dt)
-        kargs = (Hk, K.data_ptr(), ks, K_out.data_ptr(), kos)
+        for name, t in (("K", K), ("K_out", K_out)):
+            if t is not None:
+                _rows(name, t, ntok, K.shape[1], d, Q.dtype)
     else:
         _require(K_out is None, "K_out without K")
-    _call(Q.get_device(), (Q, K, Q_out, K_out, start, cu_seqlens, rp.phases), load_library().mf_rope,
-          C.byref(rp._desc), C.byref(b), d, _dtype_code(dt), Hq, Q.data_ptr(), qs,
-          Q_out.data_ptr(), qos, *kargs, int(bool(backward)))
-    return Q_out if K is None else (Q_out, K_out)
+    _refuse_the_rest(Q, K, start, cu_seqlens, Q_out, K_out, rp.phases)
 
 
 class KVCache:
@@ -655,25 +636,18 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
         return None if r is True else _made(r)
     _require(K.dim() == 3, "K must be [ntok, Hkv, d]")
     ntok, dt, d = K.shape[0], cache.K.dtype, cache.d
-    b = _batch(ntok, lens, cu_seqlens)
-    ks = _rows("K", K, ntok, cache.Hkv, d, dt)
-    vs = _rows("V", V, ntok, cache.Hkv, d, dt)
-    qargs = (0, None, 0, None, 0)
+    _batch(ntok, lens, cu_seqlens)
+    _rows("K", K, ntok, cache.Hkv, d, dt)
+    _rows("V", V, ntok, cache.Hkv, d, dt)
     if Q is not None:
         _require(Q.dim() == 3 and Q.shape[1] > 0, "Q must be [ntok, Hq, d]")
-        Hq = Q.shape[1]
-        qs = _rows("Q", Q, ntok, Hq, d, dt)
-        if Q_out is None:
-            Q_out = _new_like(Q)
-        qargs = (Hq, Q.data_ptr(), qs, Q_out.data_ptr(), _rows("Q_out", Q_out, ntok, Hq, d, dt))
+        for name, t in (("Q", Q), ("Q_out", Q_out)):
+            if t is not None:
+                _rows(name, t, ntok, Q.shape[1], d, dt)
     else:
         _require(Q_out is None, "Q_out without Q")
-    _call(cache.K.get_device(), (cache.V, cache.page_table, K, V, lens, Q, Q_out, cu_seqlens,
-                                 None if rope is None else rope.phases),
-          load_library().mf_kv_append, C.byref(cache._desc),
-          None if rope is None else C.byref(rope._desc), C.byref(b), K.data_ptr(), ks,
-          V.data_ptr(), vs, *qargs)
-    return Q_out
+    _refuse_the_rest(*cache._args, K, V, lens, Q, Q_out, cu_seqlens,
+                     None if rope is None else rope.phases)
 
 
 def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, band_width=0,
@@ -689,41 +663,29 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
         scale = cache.d ** -0.5
     f = _fast or _load_fast()
     r = f.paged_attn(cache._addr, cache._device, Q, lens, O, lse, workspace, len_add, scale,
-                         band_bias, band_width, window)
+                     band_bias, band_width, window)
     if r is not None:
         return _made(r)
-    L = load_library()
     nseq, d, dt = cache.nseq, cache.d, cache.K.dtype
     for name, x in (("len_add", len_add), ("band_width", band_width), ("window", window)):
         _require(-2 ** 31 <= x < 2 ** 31, f"{name} must fit in 32 bits")
     _require(Q.dim() == 3, "Q must be [nseq, Hq, d]")
     Hq = Q.shape[1]
-    qs = _rows("Q", Q, nseq, Hq, d, dt)
+    _rows("Q", Q, nseq, Hq, d, dt)
     _index("lens", lens, nseq)
-    if O is None:
-        O = _new_like(Q)
-    os_ = _rows("O", O, nseq, Hq, d, dt)
-    if lse is None:
-        lse = Q.new_empty((Hq, nseq), dtype=torch.float32)
-    elif lse.dtype != torch.float32 or lse.shape != (Hq, nseq) or not lse.is_contiguous():
+    if O is not None:
+        _rows("O", O, nseq, Hq, d, dt)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, nseq)
+                            or not lse.is_contiguous()):
         _refuse("lse must be a contiguous float32 tensor [Hq, nseq]")
-    a = PagedAttnDesc(Hq, scale, band_bias, band_width, window,
-                      len_add)
-    c = cache._desc
-    cr, ar = C.byref(c), C.byref(a)
-    nbytes = L.mf_paged_attn_workspace(cr, ar)
-    if nbytes == 0:  # the call finds the same error and returns its status
-        _check(L.mf_paged_attn(cr, ar, None, None, 0, None, 0, None, None, 0, None))
-    if workspace is not None and workspace.numel() >= nbytes + 256:
+    L, c = load_library(), cache._desc
+    a = PagedAttnDesc(Hq, scale, band_bias, band_width, window, len_add)
+    if L.mf_paged_attn_workspace(C.byref(c), C.byref(a)) == 0:  # says what is wrong, as the call
+        _check(L.mf_paged_attn(C.byref(c), C.byref(a), None, None, 0, None, 0, None, None, 0, None))
+    if workspace is not None:
         _require(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
                  "workspace must be a contiguous uint8 tensor")
-        wsp = workspace.data_ptr() + (-workspace.data_ptr()) % 256
-    else:
-        workspace, wsp = _workspace(nbytes, Q.device)
-    _call(Q.get_device(), (cache.K, cache.V, cache.page_table, Q, O, lens, lse, workspace),
-          L.mf_paged_attn, cr, ar, lens.data_ptr(), Q.data_ptr(), qs, O.data_ptr(), os_,
-          lse.data_ptr(), wsp, nbytes)
-    return O, lse
+    _refuse_the_rest(*cache._args, Q, lens, O, lse, workspace)
 
 
 def mapped_av_plan(Hs, Hr, Hkv):

@@ -212,3 +212,53 @@ def test_band_bias_of_any_size(dt, Hq, Hkv, d, bias, window):
                 # the sum with the bias rounds once more, at the bias's size
                 err = (lse[hs, s].double() - e).abs()
                 assert (err <= delta + 2.0 ** -22 * e.abs()).all(), (s, L)
+
+
+# ------------------------------------------------------------------ marshalling
+
+def small_calls(dev="cuda"):
+    """(function, arguments, keywords) of one valid call of each kind, and the cache."""
+    with torch.cuda.device(dev):
+        c = filled_cache([40, 17], 16, 2, 64, F32, 130)
+        rp, lens, x = mfb.Rope.make(64), i32([40, 17]), randn((2, 8, 64), F32, 131)
+        Q, K = x[:, :4], x[:, 4:6]
+        return c, [(mfb.rope, (rp, Q, K), dict(start=lens)),
+                   (mfb.rope, (rp, Q), dict(cu_seqlens=i32([0, 2]), backward=True)),
+                   (mfb.kv_append, (c, K, x[:, 6:], i32([39, 16])), dict(rope=rp, Q=Q)),
+                   (mfb.paged_attn, (c, Q, lens), dict(band_bias=1.0, band_width=3))]
+
+
+def test_a_call_is_made_in_one_place(monkeypatch):
+    """What the marshalling does not take is refused, never made some other way."""
+    c, calls = small_calls()
+    want = [f(*a, **kw) for f, a, kw in calls]
+    K0, fast = c.K.clone(), mfb._fast
+
+    class Refusing:
+        def __getattr__(self, name):
+            return fast.kv_cache if name == "kv_cache" else lambda *a: None
+
+    monkeypatch.setattr(mfb, "_fast", Refusing())
+    for f, a, kw in calls:
+        with pytest.raises(mfb.MapflowError) as e:
+            f(*a, **kw)
+        assert e.value.status == mfb.MF_ERR_INVALID_ARG and str(e.value)
+    assert torch.equal(c.K.view(torch.int32), K0.view(torch.int32))
+    monkeypatch.undo()
+    for (f, a, kw), w in zip(calls, want):
+        got = f(*a, **kw)
+        for x, y in zip(got, w) if isinstance(w, tuple) else ((got, w),):
+            assert torch.equal(x, y)
+    mfb.sync_status()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_tensors_on_another_device_than_the_current_one():
+    _, calls = small_calls("cuda:0")
+    want = [f(*a, **kw) for f, a, kw in calls]
+    _, calls = small_calls("cuda:1")
+    for (f, a, kw), w in zip(calls, want):
+        got = f(*a, **kw)
+        assert torch.cuda.current_device() == 0
+        for x, y in zip(got, w) if isinstance(w, tuple) else ((got, w),):
+            assert x.device.index == 1 and torch.equal(x.cpu(), y.cpu())
