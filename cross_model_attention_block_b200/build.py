@@ -5,7 +5,8 @@
 Objects go to cross_model_attention_block_b200/_build/, the library to
 cross_model_attention_block_b200/libmapflow.so.  A source is recompiled when it
 or any header is newer than its object.  The argument marshalling of the decode
-calls (csrc_py/, against torch's headers) becomes _marshal.so beside it.
+calls (csrc_py/, against torch's headers) becomes _marshal.so beside it, again
+whenever torch or Python are others than it was built for.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmapflow.so")
 MARSHAL_SRC = os.path.join(PKG, "csrc_py", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_FOR = os.path.join(PKG, "_build", "marshal_for")  # marshal_key() of the built one
 CUDA_HOME = os.environ.get("CUDA_HOME", "/usr/local/cuda")
 NVCC = os.path.join(CUDA_HOME, "bin", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,10 +58,27 @@ def _compile(src, obj, verbose_ptxas=False):
     return r.stderr
 
 
+def marshal_key() -> str:
+    """What _marshal.so's inlined accesses to torch's and Python's objects depend on."""
+    import sysconfig
+
+    import torch
+    return (f"torch {torch.__version__} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"{sysconfig.get_config_var('SOABI')}")
+
+
+def _marshal_stale(key: str) -> bool:
+    hdr = os.path.join(ROOT, "include", "mapflow.h")
+    if _stale(MARSHAL_SRC, MARSHAL, os.path.getmtime(hdr)) or not os.path.exists(MARSHAL_FOR):
+        return True
+    with open(MARSHAL_FOR) as f:
+        return f.read() != key
+
+
 def build_marshal(force: bool = False) -> str:
     """Compile _marshal.so against the running interpreter's torch."""
-    hdr = os.path.join(ROOT, "include", "mapflow.h")
-    if not force and not _stale(MARSHAL_SRC, MARSHAL, os.path.getmtime(hdr)):
+    key = marshal_key()
+    if not force and not _marshal_stale(key):
         return MARSHAL
     import sysconfig
 
@@ -69,7 +88,8 @@ def build_marshal(force: bool = False) -> str:
            os.path.join(CUDA_HOME, "include"), os.path.join(troot, "include"),
            os.path.join(troot, "include", "torch", "csrc", "api", "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMF_MARSHAL_KEY="{key}"']
     for i in inc:
         cmd += ["-isystem" if troot in i else "-I", i]
     tmp = MARSHAL + ".tmp"
@@ -79,6 +99,9 @@ def build_marshal(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     shutil.move(tmp, MARSHAL)
+    os.makedirs(os.path.dirname(MARSHAL_FOR), exist_ok=True)
+    with open(MARSHAL_FOR, "w") as f:
+        f.write(key)
     return MARSHAL
 
 

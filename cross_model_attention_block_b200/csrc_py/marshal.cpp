@@ -326,4 +326,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  // the torch and Python it was compiled against: another's objects may lie otherwise
+  if (m && PyModule_AddStringConstant(m, "built_for", MF_MARSHAL_KEY) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

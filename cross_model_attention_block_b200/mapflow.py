@@ -16,6 +16,8 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
+from .build import marshal_key
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # the in-tree build; MAPFLOW_LIB names another build of the same library
 LIB_PATH = os.environ.get("MAPFLOW_LIB") or os.path.join(_HERE, "libmapflow.so")
@@ -451,11 +453,14 @@ def _require(ok, msg):
 def _load_fast():
     global _fast
     L = load_library()
+    why = ("_marshal.so is missing or does not fit this torch: build it with "
+           "`python -m cross_model_attention_block_b200.build --force`")
     try:
         from . import _marshal
     except ImportError as e:
-        raise RuntimeError("_marshal.so is missing or does not fit this torch: build it with "
-                           "`python -m cross_model_attention_block_b200.build --force`") from e
+        raise RuntimeError(why) from e
+    if getattr(_marshal, "built_for", None) != marshal_key():
+        raise RuntimeError(why)
     _marshal.bind(*(C.cast(getattr(L, n), C.c_void_p).value for n in (
         "mf_rope", "mf_kv_append", "mf_paged_attn", "mf_paged_attn_workspace")))
     _fast = _marshal
