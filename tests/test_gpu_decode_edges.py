@@ -11,8 +11,8 @@ import pytest
 import torch
 
 from cross_model_attention_block_b200 import mapflow as mfb
-from tests.test_gpu_decode import (BF, F32, attend64, filled_cache, i32, near_rotated, pages, randn,
-                                   slots)
+from tests.test_gpu_decode import (BF, F32, attend64, check_attention, filled_cache, i32,
+                                   near_rotated, pages, randn, slots)
 from tests.test_gpu_decode_cuts import widened
 
 pytestmark = pytest.mark.gpu
@@ -212,6 +212,25 @@ def test_band_bias_of_any_size(dt, Hq, Hkv, d, bias, window):
                 # the sum with the bias rounds once more, at the bias's size
                 err = (lse[hs, s].double() - e).abs()
                 assert (err <= delta + 2.0 ** -22 * e.abs()).all(), (s, L)
+
+
+@pytest.mark.parametrize("dt,Hq,Hkv,d", [(BF, 8, 2, 128), (F32, 4, 2, 64)])
+def test_a_chunk_attends_through_repeated_table_rows(dt, Hq, Hkv, d):
+    """Several new tokens of a sequence: one append, then one attention over a table with the
+    sequence's row once a token, each token's own length."""
+    past, n = [700, 0], [9, 21]
+    table, npages = pages([p + m for p, m in zip(past, n)], 16, 140)
+    c = mfb.KVCache(randn((npages, 16, Hkv, d), dt, 141), randn((npages, 16, Hkv, d), dt, 142),
+                    table)
+    x, cu = randn((30, Hq + 2 * Hkv, d), dt, 143), i32([0, 9, 30])
+    Q = mfb.kv_append(c, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], i32(past), rope=mfb.Rope.make(d),
+                      Q=x[:, :Hq], cu_seqlens=cu)
+    rows = torch.repeat_interleave(torch.arange(2, device="cuda"), i32(n).long())
+    each = mfb.KVCache(c.K, c.V, table[rows].contiguous())
+    lengths = [p + 1 + i for p, m in zip(past, n) for i in range(m)]
+    O, lse = mfb.paged_attn(each, Q, i32(lengths))
+    mfb.sync_status()
+    check_attention(each, lengths, Q, O, lse, d ** -0.5)
 
 
 # ------------------------------------------------------------------ marshalling
