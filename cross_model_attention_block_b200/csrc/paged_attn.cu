@@ -24,12 +24,18 @@
 //  * A row inside one run is finished there.  Rows that a block's warps share
 //    are joined in shared memory when all are through; the pieces (maximum,
 //    sum, unnormalised O) of those that blocks share, two a block at most, go
-//    to the workspace, and a second, dependent launch joins them.  The cuts and
-//    the order of the sums depend on the lengths alone.
+//    to the workspace, and a second, dependent launch joins them.
+//
+// The cuts and the order of the sums follow from the lengths of all sequences,
+// the sizes of the pool and the table, and the heads, never from timing: a call
+// repeats its bits.  A sequence's differ (within the rounding of float32 sums)
+// beside other sequences or behind a table of another width.
 //
 // Measured (bf16, d 128, 32 heads over 8, pages of 16): 64 sequences of 1 K to
-// 16 K tokens, 1.39 GB, 217 us (6.4 TB/s); 32 K tokens 31 us, of which 2 to find
-// the cuts, 21 at 6.4 TB/s and 6 to join; 1 K tokens 9.2 us, all of it latency.
+// 16 K tokens, 1.39 GB, 217 us (6.4 TB/s).  32 K tokens 31.2 us: 1.8 to find the
+// cuts, 2.9 more until the first keys are there, 21 until the last are read (6.4
+// TB/s), 1.3 to join in the blocks, 2.3 for the second launch, 2 around them.  1 K
+// tokens 9.4 us, all latency: 1.4, 1.8, 1.3, 0.9, 1.5 and 2.4 of the same.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -302,16 +308,17 @@ struct Join {
 // finite bf16 (one instruction a register, 32 a unit at 128 dims).
 //
 // Why warp-level products: a unit's 32 take 256 cycles of an SM quarter's tensor
-// pipe, and HBM brings its two warps a unit each in 2260, so a quarter of that
-// pipe is enough (up to 48 and a third with 16 heads); operands and sums stay in
-// one warp's registers and no warp waits for another.  The same work as
+// pipe, and HBM brings its two warps a unit each in 1.48 us, 2720 cycles at the
+// 1837 MHz of such a call, so a fifth of that pipe is enough (up to 48 products
+// and three tenths with 16 heads); operands and sums stay in one warp's registers
+// and no warp waits for another.  The same work as
 // tcgen05 products of 128 keys x heads, with P through shared memory and sums
 // in TMEM, took 237 us where this took 226 then, and 48 where 17 (short
 // rows): each tile is a chain of five hand-offs, and a row's end another two.
 //
-// A unit takes a warp 1800 cycles at 4 heads a group: 350 S, 320 weights, 220
-// O, 100 waits, and 700 to issue the next copies, which the SM's TMA unit
-// takes at one in 62 cycles, 16 a round of its 8 warps.
+// A unit takes a warp 2420 cycles of the 64 sequences' call (clock64, 1837 MHz), 4
+// heads a group: 350 S, 320 weights, 250 O, 640 to issue the next copies, 110
+// between these, and 760 waiting; with keys in L2 1610, 90 of them waiting.
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -1073,7 +1080,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           add(smem + S::kOffPieces + k * S::kPiece, join_ml[0][k][h]);
         }
         if (v >= 0 && !open)
-          put_row(Finished<T, D>{p, s, r / p.groups * p.G + group * p.gh, bias_of(p, mark)}, h, acc);
+          put_row(Finished<T, D>{p, s, r / p.groups * p.G + group * p.gh, bias_of(p, mark)}, h,
+                  acc);
         else
           put_row(piece_at<D>(p, 2 * blockIdx.x + (v < 0 ? 0 : 1)), h, acc);
       }

@@ -17,7 +17,7 @@
 // their sines into shared memory, each once; then its warps walk the tokens'
 // heads (Q, K and V alike), two 16-byte packs a lane and step, and read the
 // sines where they are used.  Loads are hidden by the number of warps: six
-// blocks on an SM at 40 registers.  Measured at 32,768 tokens of 40 + 40 heads
+// blocks on an SM at 39 registers.  Measured at 32,768 tokens of 40 + 40 heads
 // of 128: sines kept in registers and four heads loaded ahead (115 registers,
 // two blocks) 317 us; two steps loaded ahead 257; as here 205 (6.6 TB/s).
 #include <algorithm>

@@ -3,7 +3,8 @@
 Every step of the path runs in the library's CUDA kernels; this module only
 turns torch tensors into pointers, allocates caller-owned outputs and
 workspaces with torch, and passes torch's current stream.  There is no CPU
-fallback: if the shared library is missing, loading raises.
+fallback: if the shared library is missing, loading raises.  Nothing here is
+recorded for autograd: outputs never require gradients, whatever the inputs do.
 
 Names follow the C ABI in include/mapflow.h.
 """
@@ -560,7 +561,8 @@ def rope(rp: Rope, Q, K=None, start=None, cu_seqlens=None, Q_out=None, K_out=Non
     Token t of sequence s (cu_seqlens [nseq + 1], int32 on the device) has position
     start[s] + t - cu_seqlens[s], and the rows of tokens past cu_seqlens[nseq] are left as
     they were; without cu_seqlens, start [ntok] holds every token's own position.
-    backward=True takes gradients of the outputs to those of the inputs.
+    backward=True takes gradients of the outputs to those of the inputs; the call does not
+    record itself for autograd.
     Q_out may be Q, and K_out may be K."""
     f = _fast or _load_fast()
     r = f.rope(rp._addr, rp._args[0], Q, K, start, cu_seqlens, Q_out, K_out, backward)
@@ -632,8 +634,8 @@ def kv_append(cache: KVCache, K, V, lens=None, rope=None, Q=None, Q_out=None, cu
     holds; rotates the same tokens' queries Q [ntok, Hq, d] and returns them (None
     without Q).  cu_seqlens [nseq + 1]: the new tokens of every sequence; None: one each.
     The rows of a padding sequence, marked by a negative length, and of tokens past
-    cu_seqlens[nseq] are left as they were.
-    `lens` itself is not changed."""
+    cu_seqlens[nseq] are left as they were.  A token without a page is not written and is
+    reported by sync_status.  `lens` itself is not changed."""
     f = _fast or _load_fast()
     r = f.kv_append(cache._addr, cache._device, K, V, lens, None if rope is None else rope._addr,
                     None if rope is None else rope._args[0], Q, Q_out, cu_seqlens)
@@ -663,7 +665,10 @@ def paged_attn(cache: KVCache, Q, lens, len_add=0, scale=None, band_bias=0.0, ba
 
     scale: 1/sqrt(d) by default; band_bias within band_width tokens, as the sender's
     logits; window: keys more than window - 1 tokens back are masked (0: none).
-    `workspace` may be a uint8 device tensor reused across calls (one per call in flight)."""
+    `workspace` may be a uint8 device tensor reused across calls (one per call in flight), of
+    256 bytes more than mf_paged_attn_workspace; with less, or without, the call allocates.
+    Several new tokens of a sequence: a cache whose page table repeats the sequence's row once
+    a token, and each token's own length."""
     if scale is None:
         scale = cache.d ** -0.5
     f = _fast or _load_fast()

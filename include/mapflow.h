@@ -471,7 +471,13 @@ mf_status mf_kv_append(const mf_kv_cache* cache, const mf_rope_desc* rope,
  * outside the pool or the table counts as masked and sets the device status
  * (MF_ERR_INVALID_ARG via mf_sync_status).  Rows of the pools past a
  * sequence's end, and keys outside the window, have no influence, whatever
- * they hold.  Results do not depend on scheduling.
+ * they hold.  The same call repeats its bits: they depend on the lengths of all
+ * sequences and on the sizes of the cache, not on scheduling.  Unnormalised sums
+ * hold weights of up to 2^8, so values of 2^120 over a sequence's length and more
+ * may overflow them.
+ * Several new tokens of a sequence (a chunk) take a call each, or one call on a
+ * cache whose page table repeats the sequence's row once a token, with each
+ * token's own length; either way the context is read once a token.
  *  ws: at least mf_paged_attn_workspace(cache, attn) bytes (device, 256-byte
  *  aligned); calls that may overlap need a workspace each.
  * Hq: a multiple of Hkv, at most 256.  Errors: MF_ERR_INVALID_ARG,
